@@ -15,7 +15,12 @@ import os
 
 __all__ = ["gdn_fwd", "gdn_fwd_train", "gdn_bwd_saved", "fwd_train", "gdn_fwd_scan", "gdn_fwd_scan_workspace_size", "fwd_scan", "gdn_fwd_recurrent", "gdn_diag_fwd", "gdn_diag_fwd_recurrent", "gdn_bwd",
            "gdn_bwd_workspace_size", "gdn_bwd_noalloc", "fwd", "fwd_recurrent", "diag_fwd", "diag_fwd_recurrent",
-           "bwd", "gated_delta_rule", "GdnError", "lib_path", "load", "version"]
+           "bwd", "gated_delta_rule", "GdnError", "lib_path", "load", "version",
+           # linear attention with a decay per head, and states in a pool
+           "gdn_linear_fwd", "gdn_linear_fwd_recurrent", "gdn_linear_bwd", "gdn_linear_workspace_size", "linear_fwd",
+           "linear_fwd_recurrent", "linear_bwd", "linear_attention", "gdn_fwd_recurrent_pool",
+           "gdn_linear_fwd_recurrent_pool", "gdn_state_move", "fwd_recurrent_pool", "linear_fwd_recurrent_pool",
+           "state_move", "StatePool"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDN_LIB_PATH names another build of the same library (the tests use it to
@@ -29,8 +34,8 @@ GDN_FLAG_NO_SEGMENTS = 1
 
 
 class GdnError(RuntimeError):
-    def __init__(self, status: int, msg: str):
-        super().__init__(f"gdn_fwd failed ({status}): {msg}")
+    def __init__(self, status: int, msg: str, call: str = "gdn_fwd"):
+        super().__init__(f"{call} failed ({status}): {msg}")
         self.status = status
 
 
@@ -78,6 +83,21 @@ def load():
         lib.gdn_bwd_noalloc.argtypes = [P] * 15 + [I] * 5 + [P, I]
         lib.gdn_bwd_workspace_size.restype = ctypes.c_longlong
         lib.gdn_bwd_workspace_size.argtypes = [I] * 6
+        LL = ctypes.c_longlong
+        lib.gdn_linear_fwd.restype = I
+        lib.gdn_linear_fwd.argtypes = [P] * 8 + [I] * 5 + [P, I, P, LL]
+        lib.gdn_linear_fwd_recurrent.restype = I
+        lib.gdn_linear_fwd_recurrent.argtypes = [P] * 8 + [I] * 5 + [P, I]
+        lib.gdn_linear_bwd.restype = I
+        lib.gdn_linear_bwd.argtypes = [P] * 12 + [I] * 5 + [P, I, P, LL]
+        lib.gdn_linear_workspace_size.restype = LL
+        lib.gdn_linear_workspace_size.argtypes = [I] * 8
+        lib.gdn_fwd_recurrent_pool.restype = I
+        lib.gdn_fwd_recurrent_pool.argtypes = [P] * 9 + [I] * 6 + [P, I]
+        lib.gdn_linear_fwd_recurrent_pool.restype = I
+        lib.gdn_linear_fwd_recurrent_pool.argtypes = [P] * 8 + [I] * 6 + [P, I]
+        lib.gdn_state_move.restype = I
+        lib.gdn_state_move.argtypes = [P, LL, LL, LL, P, P, I, P]
         lib.gdn_strerror.restype = ctypes.c_char_p
         lib.gdn_strerror.argtypes = [I]
         lib.gdn_version.restype = I
@@ -544,3 +564,9 @@ def _gdr_function():
 
         _GDR = _GatedDeltaRule
     return _GDR
+
+
+from .linear import (gdn_linear_bwd, gdn_linear_fwd, gdn_linear_fwd_recurrent,  # noqa: E402
+                     gdn_linear_workspace_size, linear_attention, linear_bwd, linear_fwd, linear_fwd_recurrent)
+from .pool import (StatePool, fwd_recurrent_pool, gdn_fwd_recurrent_pool,  # noqa: E402
+                   gdn_linear_fwd_recurrent_pool, gdn_state_move, linear_fwd_recurrent_pool, state_move)
