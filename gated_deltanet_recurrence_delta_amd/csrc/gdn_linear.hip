@@ -16,19 +16,21 @@
 // where backwards the state is met after the row's own decay, not before it:
 // out_i takes a^i S0 and S_end takes a^(n-j) y_j z_j^T.
 //
-// Chunks of 64 rows: with P = (X Y^T) . a^(i-j) (j <= i),
-//   O = P Z + diag(a^(i+1)) X S,   S <- a^64 S + (diag(a^(63-j)) Y)^T Z.
+// Chunks of C rows: with P = (X Y^T) . a^(i-j) (j <= i),
+//   O = P Z + diag(a^(i+1)) X S,   S <- a^C S + (diag(a^(C-1-j)) Y)^T Z.
 //
-// A workgroup owns a chain's tile of 32 state columns and walks the chunks.
-// X Y^T is then formed once for each 32 columns; in exchange the chain's
-// tiles give four times the workgroups, no chain has to be cut while there
-// are enough of them, and the tiles' shared rows come from their XCD's L2.
-// Each of four waves owns 16 rows of the outputs and a part of the state's
-// rows.  The scores are formed transposed, Y X^T, so that their accumulators
-// are the second product's operand as they stand; the state's accumulators
-// are the third's, and go round through LDS once a chunk because each wave
-// needs all of them.  A fifth wave copies the chunks to LDS, and one barrier
-// a chunk hands them and the state over.
+// A workgroup walks the chunks of one chain (or of a segment of it) with the
+// whole state in registers: each computing wave owns 16 state columns, all
+// dx rows of them, so the state's accumulators are the outputs' operand as
+// they stand and nothing of the state goes through LDS.  The scores are
+// formed transposed, Y X^T, so that their accumulators are an operand too;
+// their 16 x 16 blocks are shared out among the waves and handed over
+// through LDS.  One more wave copies the chunks of x, y and z to LDS, two
+// chunks ahead: every row is read from memory once, and the matrix cores
+// have four times the time that the products need at dx = dz = 128.
+// (Workgroups of 32 state columns each, four to a chain, need no segments at
+// 64 chains, but read x and y four times over: from L2 that goes at 11 TB/s,
+// and B=4 H=16 T=4096 took 98 us that way.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -39,10 +41,6 @@
 #include "gdn_linear.h"
 
 namespace {
-
-constexpr int C = 64;    // rows of a chunk
-constexpr int ZT = 32;   // state columns of a workgroup
-constexpr int NWC = 4;   // computing waves
 
 struct Role {
   const char* x;
@@ -60,35 +58,44 @@ struct LinParams {
   const float* g;
   const int32_t* cu;  // null: dense
   f32x4* ws;          // end states of the segments
-  int B, T, H, nrole, tiles;
+  int B, T, H, nrole;
   int segc;           // chunks of a segment; 0: nothing is cut
-  int nslot;          // segment slots: of a dense sequence, or of the packed batch
+  int nslots;         // (sequence, segment) slots
+  int nseg;           // of them a dense sequence's
 };
 
-template <typename TI, int DX>
+template <typename TI, int DX, int DZ, int PASS>
 struct LK {
   using Frag = typename Mma<TI>::frag;
   static constexpr bool B16 = sizeof(TI) == 2;
   static constexpr int ES = sizeof(TI), SLAB = Mma<TI>::SLAB, E = Mma<TI>::E;
-  static constexpr int GR = DX * ES / 16, ZGR = ZT * ES / 16;  // 16-byte granules of a row
-  static constexpr int NS = DX / SLAB, NJS = C / SLAB;
-  static constexpr int YB = C * DX * ES, ZB = C * ZT * ES, MB = NS * 2 * 1024;
-  static constexpr int Y_INS = YB / 1024, Z_INS = ZB / 1024;
-  static constexpr int NBUF = 3 * (YB + ZB) + 2 * MB <= 80 * 1024 ? 3 : 2;
-  // State tiles of a wave: SPW slabs of x rows, ZPW 16-column blocks, TPS
-  // accumulators a slab.
-  static constexpr int SPW = NS >= 4 ? NS / 4 : 1, ZPW = NS >= 4 ? 2 : 1, TPS = SLAB / 16;
-  static constexpr int NU = SPW * ZPW * TPS;
-  __device__ static inline int slab_of(int w, int i) { return NS >= 4 ? w * SPW + i : (NS == 2 ? w >> 1 : 0); }
-  __device__ static inline int zb_of(int w, int i) { return NS >= 4 ? i : w & 1; }
-  __device__ static inline bool has_state(int w) { return NS > 1 || w < 2; }
-  // Accumulator row 4 q + e of state tile t of a slab: with two tiles a slab
-  // a lane's eight rows are neighbours, as a fragment wants them.
-  __device__ static inline int x_of(int t, int q) { return B16 ? 8 * q + 4 * t : 4 * q; }
-  // State column of MFMA row or column m of block zb: a lane's output columns are neighbours.
-  __device__ static inline int z_of(int zb, int m) { return B16 ? 8 * (m >> 2) + 4 * zb + (m & 3) : 16 * zb + m; }
+  static constexpr int C = B16 ? 64 : 32, NB = C / 16;         // rows of a chunk, 16-row blocks
+  static constexpr int NW = DZ / 16, NT = 64 * (NW + 1);       // computing waves, threads
+  static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
+  static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
+  // LDS: NBUF chunks of (x,) y and z, the scores, their decays.  Two
+  // workgroups on a CU where that leaves two chunks each, else three chunks.
+  static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, XB = PASS == 0 ? YB : 0, SB = XB + YB + ZB;
+  static constexpr int PB = PASS == 0 ? NB * NJS * 1024 : 0, DB = PASS == 0 ? NB * 1024 : 0;
+  static constexpr int NBUF = 3 * SB + PB + DB <= 79 * 1024 || 2 * SB + PB + DB > 79 * 1024 ? 3 : 2;
+  static constexpr int LDS = NBUF * SB + PB + DB;
+  static constexpr int X_INS = XB / 1024, Y_INS = YB / 1024, Z_INS = ZB / 1024, INS = X_INS + Y_INS + Z_INS;
+  static_assert((NBUF - 2) * INS < 64, "copies in flight are counted in six bits");
+  // In 16-bit storage a transposing read takes four neighbouring values of a
+  // row, half a granule.  The halves alternate from granule to granule, so
+  // that a read covers all banks: accumulator row m = 4 q + e of tile t of a
+  // slab is x value 8 q + 4 (t ^ (q & 1)) + e, and a lane's eight values of
+  // two tiles are neighbours.
+  __device__ static inline int half_of(int t, int q) { return 4 * (t ^ (q & 1)); }
+  __device__ static inline int x_of(int t, int q) { return B16 ? 8 * q + half_of(t, q) : 4 * q; }
   __device__ static inline int swz_y(int r) { return swz_kq<GR>(r); }
-  __device__ static inline int swz_z(int r) { return B16 ? (r >> 1) & 3 : 0; }
+  // A transposing read of z takes 32 bytes of each of eight rows.
+  __device__ static inline int swz_z(int r) {
+    if constexpr (!B16) return 0;
+    else if constexpr (ZGR >= 16) return 8 * (r & 1) + 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1);
+    else if constexpr (ZGR >= 8) return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1);
+    else return 2 * ((r >> 2) & 1);
+  }
 };
 
 // exp(n g), and what its rounding to 32 bits leaves: a constant factor's
@@ -113,412 +120,492 @@ __device__ static inline V buf_load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// PASS 0: outputs (and end states); PASS 1: the end states of the segments
-// that others follow, each from zero (a sequence's first from S0).
-template <typename TI, int DX, int PASS>
-__global__ __launch_bounds__(64 * (NWC + 1)) void linear_kernel(const LinParams p) {
-  using K = LK<TI, DX>;
+// Where a workgroup's chain and segment lie.
+struct Span {
+  long th0;  // token-head of the sequence's first row
+  int n, seg, slot, h, ri, len, nch, c0, c1;
+};
+
+// Rows further back than this many nats of decay are left out of a segment's
+// end state: e^-60 of their own share, far below what 32 bits can add up.
+constexpr double FORGOTTEN = 60.0;
+
+// A computing wave's part.
+template <typename TI, int DX, int DZ, int PASS>
+__device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds,
+                                      const double* sPow) {
+  using K = LK<TI, DX, DZ, PASS>;
   using Frag = typename K::Frag;
-  __shared__ __attribute__((aligned(16))) char sY[K::NBUF * K::YB];
-  __shared__ __attribute__((aligned(16))) char sZ[K::NBUF * K::ZB];
-  __shared__ __attribute__((aligned(16))) char sM[PASS == 0 ? 2 * K::MB : 16];
-  __shared__ double sPow[C + 1];
-  __shared__ int sSeq;
+  constexpr int C = K::C;
+  const Role& role = p.role[sp.ri];
+  const int lane = threadIdx.x & 63, m16 = lane & 15, q4 = lane >> 4;
+  const int H = p.H, rev = role.reverse, len = sp.len;
+  char* const sP = lds + K::NBUF * K::SB;
+  char* const sD = sP + K::PB;
+  const int z_at = 16 * w + m16;  // the lane's state column
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int H = p.H, DZ = p.tiles * ZT;
-
-  // ---- which chain, segment, role and tile
-  const int item = xcd_remap(blockIdx.x, gridDim.x);
-  const int tile = item % p.tiles, ri = item / p.tiles % p.nrole;
-  const int sh = item / p.tiles / p.nrole, h = sh % H, slot = sh / H;
-  const Role role = p.role[ri];
-  int n, seg;
-  if (!p.cu || p.segc == 0) {
-    const int per = p.segc ? p.nslot : 1;
-    n = slot / per;
-    seg = slot % per;
-  } else {
-    // Packed and cut: sequence n has slots floor(begin / rows of a segment) + n and on.
-    if (tid == 0) sSeq = -1;
-    __syncthreads();
-    const int rows = p.segc * C;
-    for (int i = tid; i < p.B; i += 64 * (NWC + 1)) {
-      const int b = min(max(p.cu[i], 0), p.T), e = min(max(p.cu[i + 1], b), p.T);
-      const int first = b / rows + i, count = max(1, (e - b + rows - 1) / rows);
-      if (slot >= first && slot < first + count) sSeq = i;
-    }
-    __syncthreads();
-    n = sSeq;
-    if (n < 0) return;
-    seg = slot - (min(max(p.cu[n], 0), p.T) / rows + n);
-  }
-  long row0;
-  int len;
-  if (p.cu) {
-    const int b = min(max(p.cu[n], 0), p.T), e = min(max(p.cu[n + 1], b), p.T);
-    row0 = b;
-    len = e - b;
-  } else {
-    row0 = (long)n * p.T;
-    len = p.T;
-  }
-  const int nch = (len + C - 1) / C;
-  const int c0 = seg * p.segc, c1 = p.segc ? min(nch, c0 + p.segc) : nch;
-  if (seg > 0 && c0 >= nch) return;
-  if (PASS == 1 && c1 >= nch) return;  // nothing follows
-
-  const float gh = p.g[h];
-  if (tid <= C) sPow[tid] = pow_of(gh, tid);
-  __syncthreads();
-
-  const long th0 = row0 * H + h;  // token-head of the sequence's first row
-  const int rev = role.reverse;
-  const int x_stride = H * DX * K::ES, z_stride = H * DZ * K::ES;
-
-  if (wave == NWC) {
-    // ------------------------------------------------------------- loader --
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(role.y + th0 * DX * K::ES, (long)(len - 1) * x_stride + DX * K::ES);
-    const __amdgpu_buffer_rsrc_t rz =
-        make_rsrc(role.z + (th0 * DZ + tile * ZT) * K::ES, (long)(len - 1) * z_stride + ZT * K::ES);
-    int y_off[K::Y_INS], z_off[K::Z_INS];
-#pragma unroll
-    for (int i = 0; i < K::Y_INS; ++i) {
-      const int G = i * 64 + lane, r = G / K::GR;
-      y_off[i] = (rev ? -r : r) * x_stride + ((G % K::GR) ^ K::swz_y(r)) * 16;
-    }
-#pragma unroll
-    for (int i = 0; i < K::Z_INS; ++i) {
-      const int G = i * 64 + lane, r = G / K::ZGR;
-      z_off[i] = (rev ? -r : r) * z_stride + ((G % K::ZGR) ^ K::swz_z(r)) * 16;
-    }
-    // Rows outside the sequence lie outside the descriptors (a negative
-    // offset wraps far behind them) and read as zeros; so do the chunks
-    // behind the last, asked for to keep the count of copies even.
-    auto issue = [&](int c) {
-      const int s = (c - c0) % K::NBUF;
-      const unsigned at = rev ? (unsigned)(len - 1) - (unsigned)c * C : (unsigned)c * C;
-      const unsigned ya = at * (unsigned)x_stride, za = at * (unsigned)z_stride;
-#pragma unroll
-      for (int i = 0; i < K::Y_INS; ++i)
-        copy_to_lds(ry, sY + s * K::YB + i * 1024, c < c1 ? (int)(ya + (unsigned)y_off[i]) : -16);
-#pragma unroll
-      for (int i = 0; i < K::Z_INS; ++i)
-        copy_to_lds(rz, sZ + s * K::ZB + i * 1024, c < c1 ? (int)(za + (unsigned)z_off[i]) : -16);
-    };
-    constexpr int INS = K::Y_INS + K::Z_INS;
-    if (c0 < c1) {
-#pragma unroll
-      for (int i = 0; i < K::NBUF - 1; ++i) issue(c0 + i);
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * INS));
-    }
-    lds_barrier();
-    for (int c = c0; c < c1; ++c) {
-      issue(c + K::NBUF - 1);
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * INS));
-      lds_barrier();
-    }
-    return;
-  }
-
-  // ----------------------------------------------------------- computing --
-  const int w = wave, m16 = lane & 15, q4 = lane >> 4;
-  const int off = rev;  // the state's powers are one lower backwards, the inputs' one higher
-
-  // The state.
+  // The state: tile u has x rows x_at(u) and on.
   f32x4 M[K::NU];
+  auto x_at = [&](int u) { return u / K::TPS * K::SLAB + K::x_of(u % K::TPS, q4); };
+  auto ws_at = [&](int sl) {
+    return p.ws + (((long)sl * H + sp.h) * p.nrole + sp.ri) * (DX * DZ / 4) + w * K::NU * 64 + lane;
+  };
 #pragma unroll
   for (int u = 0; u < K::NU; ++u) M[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto at_state = [&](int u, int e, int& x, int& z) {
-    const int si = u / (K::ZPW * K::TPS), zi = u / K::TPS % K::ZPW, t = u % K::TPS;
-    x = K::slab_of(w, si) * K::SLAB + K::x_of(t, q4) + e;
-    z = tile * ZT + K::z_of(K::zb_of(w, zi), m16);
-  };
-  const bool has = K::has_state(w);
-  auto load_s0 = [&]() {
-    const float* s0 = role.s0 + ((long)n * H + h) * DX * DZ;
+  if (sp.c0 == 0) {
+    if (role.s0) {
+      const float* s0 = role.s0 + ((long)sp.n * H + sp.h) * DX * DZ;
 #pragma unroll
-    for (int u = 0; u < K::NU; ++u)
+      for (int u = 0; u < K::NU; ++u) {
+        if (role.s0_transposed) {
+          M[u] = *reinterpret_cast<const f32x4*>(s0 + z_at * DX + x_at(u));
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int x, z;
-        at_state(u, e, x, z);
-        M[u][e] = s0[role.s0_transposed ? z * DX + x : x * DZ + z];
-      }
-  };
-  auto ws_at = [&](int sl) { return p.ws + ((((long)sl * H + h) * p.nrole + ri) * p.tiles + tile) * (DX * ZT / 4); };
-  if (has) {
-    if (seg == 0) {
-      if (role.s0) load_s0();
-    } else if (PASS == 0) {
-      const Pow step = split_pow(pow_of(gh, (long)p.segc * C));
-      for (int s = slot - seg; s < slot; ++s) {
-        const f32x4* src = ws_at(s) + w * 64 * K::NU + lane;
-#pragma unroll
-        for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], step) + src[u * 64];
+          for (int e = 0; e < 4; ++e) M[u][e] = s0[(x_at(u) + e) * DZ + z_at];
+        }
       }
     }
+  } else if (PASS == 0) {
+    const Pow a = split_pow(pow_of(gh, (long)p.segc * C));
+    const double nats = -(double)gh * p.segc * C;
+    const int first = nats * sp.seg > FORGOTTEN ? max(sp.slot - sp.seg, sp.slot - 1 - (int)(FORGOTTEN / nats))
+                                                : sp.slot - sp.seg;
+    for (int s = first; s < sp.slot; ++s) {
+      const f32x4* src = ws_at(s);
+#pragma unroll
+      for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], a) + src[u * 64];
+    }
   }
-  auto publish = [&](int buf) {
-    if (!has) return;
-#pragma unroll
-    for (int si = 0; si < K::SPW; ++si)
-#pragma unroll
-      for (int zi = 0; zi < K::ZPW; ++zi) {
-        const int u = (si * K::ZPW + zi) * K::TPS;
-        lds_st(sM + buf * K::MB, ((K::slab_of(w, si) * 2 + K::zb_of(w, zi)) * 64 + lane) * 16,
-               Mma<TI>::from_acc(M[u], M[u + K::TPS - 1]));
-      }
-  };
 
-  // Powers of the decay: the scores' (row i = 16 w + m16, column j = 16 jb +
-  // 4 q4 + e), the state's at row i, the inputs' at row j.
-  f32x4 D[4], W[4];
-  float gam = 0.f;
+  // Powers of the decay: the state's at output row i = 16 ib + m16, the
+  // inputs' at row j = 16 jb + 4 q4 + e.  Backwards the state's are one lower
+  // and the inputs' one higher.
+  f32x4 Wj[K::NB];
+  float gam[K::NB];
   auto input_powers = [&](int rows) {
 #pragma unroll
-    for (int jb = 0; jb < 4; ++jb)
+    for (int jb = 0; jb < K::NB; ++jb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int d = rows - 1 - (16 * jb + 4 * q4 + e) + off;
-        W[jb][e] = d >= 0 ? (float)sPow[d] : 0.f;
+        const int d = rows - 1 - (16 * jb + 4 * q4 + e) + rev;
+        Wj[jb][e] = d >= 0 ? (float)sPow[d] : 0.f;
       }
   };
-  if constexpr (PASS == 0) {
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = 16 * (w - jb) + m16 - 4 * q4 - e;
-        D[jb][e] = d >= 0 ? (float)sPow[d] : 0.f;
-      }
-    gam = (float)sPow[16 * w + m16 + 1 - off];
-  }
   input_powers(C);
   Pow step = split_pow(sPow[C]);
-
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(role.x + th0 * DX * K::ES, (long)(len - 1) * x_stride + DX * K::ES);
-  const __amdgpu_buffer_rsrc_t ro =
-      make_rsrc(role.out + (th0 * DZ + tile * ZT) * K::ES, (long)(len - 1) * z_stride + ZT * K::ES);
-  auto row_of = [&](int c) {
-    const unsigned i = (unsigned)c * C + 16 * w + m16;
-    return rev ? (unsigned)(len - 1) - i : i;
-  };
-  Frag X[K::NS], Xn[K::NS];
-  auto load_x = [&](int c, Frag* x) {
-    const unsigned r = row_of(c) * (unsigned)x_stride + K::E * K::ES * q4;
-#pragma unroll
-    for (int s = 0; s < K::NS; ++s) x[s] = buf_load16<Frag>(rx, (int)(r + s * K::SLAB * K::ES));
-  };
+  const int z_stride = H * DZ * K::ES;
+  const __amdgpu_buffer_rsrc_t ro = make_rsrc(role.out + sp.th0 * DZ * K::ES, (long)(len - 1) * z_stride + DZ * K::ES);
+  unsigned o_off = 0;
+  const unsigned o_step = (unsigned)(rev ? -C : C) * (unsigned)z_stride;
+  const unsigned o_blk = (unsigned)(rev ? -16 : 16) * (unsigned)z_stride;
   if constexpr (PASS == 0) {
-    if (c0 < c1) load_x(c0, X);
-    publish(0);
+#pragma unroll
+    for (int ib = 0; ib < K::NB; ++ib) gam[ib] = (float)sPow[16 * ib + m16 + 1 - rev];
+    const unsigned i = (unsigned)sp.c0 * C + m16;
+    o_off = (rev ? (unsigned)(len - 1) - i : i) * (unsigned)z_stride + (16 * w + 4 * q4) * K::ES;
+    // The decays of a block of scores (row i = 16 ib + m16, column j = 16 jb
+    // + 4 q4 + e), by ib - jb; and the zeros beside the diagonal blocks.
+    for (int d = w; d < K::NB; d += K::NW) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = 16 * d + m16 - 4 * q4 - e;
+        v[e] = n >= 0 ? (float)sPow[n] : 0.f;
+      }
+      lds_st(sD, (d * 64 + lane) * 16, v);
+    }
+    for (int f = w; f < K::NB * K::NJS; f += K::NW) lds_st(sP, (f * 64 + lane) * 16, f32x4{0.f, 0.f, 0.f, 0.f});
   }
   lds_barrier();
 
-  for (int c = c0; c < c1; ++c) {
-    const char* bY = sY + (c - c0) % K::NBUF * K::YB;
-    const char* bZ = sZ + (c - c0) % K::NBUF * K::ZB;
-    if (PASS == 0 && c + 1 < c1) load_x(c + 1, Xn);
+  const int tr_r = 4 * q4 + (m16 >> 2), tr_g = m16 & 3;
+  int slot = 0;
+  for (int c = sp.c0; c < sp.c1; ++c) {
+    const char* bX = lds + slot * K::SB;
+    const char* bY = bX + K::XB;
+    const char* bZ = bY + K::YB;
+    slot = slot + 1 == K::NBUF ? 0 : slot + 1;
 
     // z columns as fragments over the rows (for two 16-row blocks: rows 4 q4
     // and on of the first, then of the second, as the scores' accumulators lie)
-    Frag Zf[2][K::NJS];
+    Frag Zf[K::NJS];
 #pragma unroll
-    for (int zb = 0; zb < 2; ++zb)
-#pragma unroll
-      for (int js = 0; js < K::NJS; ++js) {
-        if constexpr (K::B16) {
-          const int r = 32 * js + 4 * q4 + (m16 >> 2), g = m16 & 3;
-          const bf16x4 lo = lds_read_tr(bZ, r * 64 + ((g ^ K::swz_z(r)) * 16) + 8 * zb);
-          const bf16x4 hi = lds_read_tr(bZ, (r + 16) * 64 + ((g ^ K::swz_z(r + 16)) * 16) + 8 * zb);
-          Zf[zb][js] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            Zf[zb][js][e] = lds_ld<float>(bZ, ((16 * js + 4 * q4 + e) * ZT + K::z_of(zb, m16)) * 4);
-        }
-      }
-
-    if constexpr (PASS == 0) {
-      // scores, transposed and masked
-      f32x4 P[4];
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        P[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (jb <= w) {
-          const int r = 16 * jb + m16;
-#pragma unroll
-          for (int s = 0; s < K::NS; ++s) {
-            const Frag y = lds_ld<Frag>(bY, r * (K::GR * 16) + (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(r)) * 16);
-            P[jb] = Mma<TI>::mma(y, X[s], P[jb]);
-          }
-          P[jb] *= D[jb];
-        }
-      }
-      // outputs, transposed: the state's part, then the chunk's own
-      f32x4 O[2];
-      const char* bM = sM + ((c - c0) & 1) * K::MB;
-#pragma unroll
-      for (int zb = 0; zb < 2; ++zb) {
-        O[zb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < K::NS; ++s)
-          O[zb] = Mma<TI>::mma(lds_ld<Frag>(bM, ((s * 2 + zb) * 64 + lane) * 16), X[s], O[zb]);
-        O[zb] *= gam;
-#pragma unroll
-        for (int js = 0; js < K::NJS; ++js)
-          if (js * K::TPS <= w)
-            O[zb] = Mma<TI>::mma(Zf[zb][js], Mma<TI>::from_acc(P[js * K::TPS], P[js * K::TPS + K::TPS - 1]), O[zb]);
-      }
-      const unsigned at = row_of(c) * (unsigned)z_stride;
+    for (int js = 0; js < K::NJS; ++js) {
       if constexpr (K::B16) {
-        const u32x2 lo = __builtin_bit_cast(u32x2, cvt4(O[0])), hi = __builtin_bit_cast(u32x2, cvt4(O[1]));
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], lo[1], hi[0], hi[1]}, ro, (int)(at + 16 * q4), 0, 0);
+        const char* at = bZ + tr_r * (K::ZGR * 16) + (((2 * w + (tr_g >> 1)) ^ K::swz_z(tr_r)) * 16) + 8 * (tr_g & 1);
+        const bf16x4 lo = lds_read_tr(at, 32 * js * (K::ZGR * 16));
+        const bf16x4 hi = lds_read_tr(at, (32 * js + 16) * (K::ZGR * 16));
+        Zf[js] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       } else {
 #pragma unroll
-        for (int zb = 0; zb < 2; ++zb)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[zb]), ro, (int)(at + 64 * zb + 16 * q4),
-                                                 0, 0);
+        for (int e = 0; e < 4; ++e) Zf[js][e] = lds_ld<float>(bZ, ((16 * js + 4 * q4 + e) * DZ + z_at) * 4);
       }
     }
 
-    // the state: decayed rows y z^T; in 16-bit storage the decayed z are taken as two terms
-    if (has) {
-      const int rows = len - c * C;
-      if (rows < C) {  // the last chunk
-        input_powers(rows);
-        step = split_pow(sPow[rows]);
+    f32x4 O[K::NB];
+    if constexpr (PASS == 0) {
+      // this wave's blocks of scores, transposed and masked
+      const int x_row = m16 * (K::GR * 16);
+      for (int b = w; b < K::NB * (K::NB + 1) / 2; b += K::NW) {
+        int ib = 0, jb = b;
+        while (jb > ib) jb -= ++ib;
+        f32x4 P = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < K::NS; ++s) {
+          const int g = (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16;
+          P = Mma<TI>::mma(lds_ld<Frag>(bY + 16 * jb * (K::GR * 16), x_row + g),
+                           lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + g), P);
+        }
+        P *= lds_ld<f32x4>(sD, ((ib - jb) * 64 + lane) * 16);
+        char* at = sP + ((ib * K::NJS + jb / K::TPS) * 64 + lane) * 16;
+        if constexpr (K::B16) lds_st(at, 8 * (jb & 1), cvt4(P));
+        else lds_st(at, 0, P);
+      }
+      // the state's part of the outputs, transposed
+      Frag Mf[K::NS];
+#pragma unroll
+      for (int s = 0; s < K::NS; ++s) {
+        if constexpr (K::B16) {
+          const u32x2 a = __builtin_bit_cast(u32x2, cvt4(M[2 * s])), b = __builtin_bit_cast(u32x2, cvt4(M[2 * s + 1]));
+          const bool odd = q4 & 1;  // tile 0 has the lane's upper four rows
+          Mf[s] = __builtin_bit_cast(
+              Frag, u32x4{odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? a[0] : b[0], odd ? a[1] : b[1]});
+        } else {
+          Mf[s] = M[s];
+        }
       }
 #pragma unroll
-      for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], step);
-      Frag Zh[K::ZPW][K::NJS], Zl[K::ZPW][K::NJS];
+      for (int ib = 0; ib < K::NB; ++ib) {
+        O[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int zi = 0; zi < K::ZPW; ++zi)
+        for (int s = 0; s < K::NS; ++s) {
+          const int g = (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16;
+          O[ib] = Mma<TI>::mma(Mf[s], lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + g), O[ib]);
+        }
+        O[ib] *= gam[ib];
+      }
+      lds_barrier();  // the scores are there
+      // the chunk's own part
 #pragma unroll
-        for (int js = 0; js < K::NJS; ++js) {
-          Frag zf = Zf[zi][js];
-          if constexpr (K::ZPW == 1) {
+      for (int ib = 0; ib < K::NB; ++ib) {
 #pragma unroll
-            for (int e = 0; e < K::E; ++e) zf[e] = K::zb_of(w, 0) ? Zf[1][js][e] : Zf[0][js][e];
+        for (int js = 0; js * K::TPS <= ib; ++js)
+          O[ib] = Mma<TI>::mma(Zf[js], lds_ld<Frag>(sP, ((ib * K::NJS + js) * 64 + lane) * 16), O[ib]);
+        if constexpr (K::B16)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, cvt4(O[ib])), ro, (int)(o_off + ib * o_blk), 0,
+                                                0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ib]), ro, (int)(o_off + ib * o_blk), 0, 0);
+      }
+      o_off += o_step;
+    }
+
+    // the state: decayed rows y z^T; in 16-bit storage the decayed z are
+    // taken as three terms, their 24 bits in full
+    if (len - c * C < C) {  // the last chunk
+      input_powers(len - c * C);
+      step = split_pow(sPow[len - c * C]);
+    }
+#pragma unroll
+    for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], step);
+#pragma unroll
+    for (int js = 0; js < K::NJS; ++js) {
+      constexpr int TERMS = K::B16 ? 3 : 1;
+      Frag zt[TERMS];
+      if constexpr (K::B16) {
+        f32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[e] = (float)Zf[js][e] * Wj[2 * js][e];
+          b[e] = (float)Zf[js][4 + e] * Wj[2 * js + 1][e];
+        }
+#pragma unroll
+        for (int i = 0; i < TERMS; ++i) {
+          zt[i] = Mma<TI>::from_acc(a, b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] -= (float)zt[i][e];
+            b[e] -= (float)zt[i][4 + e];
           }
-          if constexpr (K::B16) {
-            f32x4 a, b;
+        }
+      } else {
+        zt[0] = Zf[js] * Wj[js];
+      }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[e] = (float)zf[e] * W[2 * js][e];
-              b[e] = (float)zf[4 + e] * W[2 * js + 1][e];
-            }
-            Zh[zi][js] = Mma<TI>::from_acc(a, b);
-            f32x4 ra, rb;
+      for (int u = 0; u < K::NU; ++u) {
+        Frag y;
+        if constexpr (K::B16) {
+          const char* at = bY + tr_r * (K::GR * 16) + (((4 * (u / 2) + tr_g) ^ K::swz_y(tr_r)) * 16) +
+                           2 * K::half_of(u & 1, tr_g);
+          const bf16x4 lo = lds_read_tr(at, 32 * js * (K::GR * 16));
+          const bf16x4 hi = lds_read_tr(at, (32 * js + 16) * (K::GR * 16));
+          y = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+          const int x = u * 16 + m16;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              ra[e] = a[e] - (float)Zh[zi][js][e];
-              rb[e] = b[e] - (float)Zh[zi][js][4 + e];
-            }
-            Zl[zi][js] = Mma<TI>::from_acc(ra, rb);
-          } else {
-            Zh[zi][js] = zf * W[js];
+          for (int e = 0; e < 4; ++e) {
+            const int r = 16 * js + 4 * q4 + e;
+            y[e] = lds_ld<float>(bY, r * (K::GR * 16) + (((x >> 2) ^ K::swz_y(r)) * 16) + (x & 3) * 4);
           }
         }
 #pragma unroll
-      for (int si = 0; si < K::SPW; ++si)
-#pragma unroll
-        for (int t = 0; t < K::TPS; ++t)
-#pragma unroll
-          for (int js = 0; js < K::NJS; ++js) {
-            Frag y;
-            if constexpr (K::B16) {
-              const int r = 32 * js + 4 * q4 + (m16 >> 2), g = 4 * K::slab_of(w, si) + (m16 & 3);
-              const bf16x4 lo = lds_read_tr(bY, r * (K::GR * 16) + ((g ^ K::swz_y(r)) * 16) + 8 * t);
-              const bf16x4 hi = lds_read_tr(bY, (r + 16) * (K::GR * 16) + ((g ^ K::swz_y(r + 16)) * 16) + 8 * t);
-              y = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            } else {
-              const int x = K::slab_of(w, si) * 16 + m16;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = 16 * js + 4 * q4 + e;
-                y[e] = lds_ld<float>(bY, r * (K::GR * 16) + (((x >> 2) ^ K::swz_y(r)) * 16) + (x & 3) * 4);
-              }
-            }
-#pragma unroll
-            for (int zi = 0; zi < K::ZPW; ++zi) {
-              const int u = (si * K::ZPW + zi) * K::TPS + t;
-              M[u] = Mma<TI>::mma(y, Zh[zi][js], M[u]);
-              if constexpr (K::B16) M[u] = Mma<TI>::mma(y, Zl[zi][js], M[u]);
-            }
-          }
-    }
-    if constexpr (PASS == 0) {
-      publish((c - c0 + 1) & 1);
-#pragma unroll
-      for (int s = 0; s < K::NS; ++s) X[s] = Xn[s];
+        for (int i = TERMS - 1; i >= 0; --i) M[u] = Mma<TI>::mma(y, zt[i], M[u]);
+      }
     }
     lds_barrier();
   }
 
-  if (!has) return;
   if constexpr (PASS == 1) {
-    f32x4* dst = ws_at(slot) + w * 64 * K::NU + lane;
+    f32x4* dst = ws_at(sp.slot);
 #pragma unroll
     for (int u = 0; u < K::NU; ++u) dst[u * 64] = M[u];
-  } else if (role.sT && c1 >= nch) {
-    float* sT = role.sT + ((long)n * H + h) * DX * DZ;
+  } else if (role.sT && sp.c1 >= sp.nch) {
+    float* sT = role.sT + ((long)sp.n * H + sp.h) * DX * DZ;
 #pragma unroll
     for (int u = 0; u < K::NU; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int x, z;
-        at_state(u, e, x, z);
-        sT[x * DZ + z] = M[u][e];
-      }
+      for (int e = 0; e < 4; ++e) sT[(x_at(u) + e) * DZ + z_at] = M[u][e];
   }
+}
+
+// The copying wave's part: chunks of x, y and z to LDS, NBUF - 1 ahead.
+template <typename TI, int DX, int DZ, int PASS>
+__device__ static inline void copy_chunks(const LinParams& p, const Span& sp, char* lds) {
+  using K = LK<TI, DX, DZ, PASS>;
+  constexpr int C = K::C;
+  const Role& role = p.role[sp.ri];
+  const int lane = threadIdx.x & 63, rev = role.reverse, len = sp.len;
+  const int y_stride = p.H * DX * K::ES, z_stride = p.H * DZ * K::ES;
+  const long y_bytes = (long)(len - 1) * y_stride + DX * K::ES;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(role.x + sp.th0 * DX * K::ES, y_bytes);
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(role.y + sp.th0 * DX * K::ES, y_bytes);
+  const __amdgpu_buffer_rsrc_t rz =
+      make_rsrc(role.z + sp.th0 * DZ * K::ES, (long)(len - 1) * z_stride + DZ * K::ES);
+  int y_off[K::Y_INS], z_off[K::Z_INS];
+#pragma unroll
+  for (int i = 0; i < K::Y_INS; ++i) {
+    const int G = i * 64 + lane, r = G / K::GR;
+    y_off[i] = (rev ? -r : r) * y_stride + ((G % K::GR) ^ K::swz_y(r)) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < K::Z_INS; ++i) {
+    const int G = i * 64 + lane, r = G / K::ZGR;
+    z_off[i] = (rev ? -r : r) * z_stride + ((G % K::ZGR) ^ K::swz_z(r)) * 16;
+  }
+  // Rows outside the sequence lie outside the descriptors (a negative offset
+  // wraps far behind them) and read as zeros; so do the chunks behind the
+  // last, asked for to keep the count of copies even.
+  int slot = 0;
+  auto issue = [&](int c) {
+    char* d = lds + slot * K::SB;
+    slot = slot + 1 == K::NBUF ? 0 : slot + 1;
+    const unsigned at = rev ? (unsigned)(len - 1) - (unsigned)c * C : (unsigned)c * C;
+    const unsigned ya = at * (unsigned)y_stride, za = at * (unsigned)z_stride;
+    const bool in = c < sp.c1;
+#pragma unroll
+    for (int i = 0; i < K::X_INS; ++i) copy_to_lds(rx, d + i * 1024, in ? (int)(ya + (unsigned)y_off[i]) : -16);
+    d += K::XB;
+#pragma unroll
+    for (int i = 0; i < K::Y_INS; ++i) copy_to_lds(ry, d + i * 1024, in ? (int)(ya + (unsigned)y_off[i]) : -16);
+    d += K::YB;
+#pragma unroll
+    for (int i = 0; i < K::Z_INS; ++i) copy_to_lds(rz, d + i * 1024, in ? (int)(za + (unsigned)z_off[i]) : -16);
+  };
+  if (sp.c0 < sp.c1) {
+#pragma unroll
+    for (int i = 0; i < K::NBUF - 1; ++i) issue(sp.c0 + i);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::INS));
+  }
+  lds_barrier();
+  for (int c = sp.c0; c < sp.c1; ++c) {
+    issue(c + K::NBUF - 1);
+    if constexpr (PASS == 0) lds_barrier();  // the scores are there
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::INS));
+    lds_barrier();
+  }
+}
+
+constexpr int SORTED = 512;  // sequences of a packed batch that are put in order of length
+
+// The (sequence, segment) of a packed batch that comes at place `at`: whole
+// segments first, then the sequences' last ones from long to short, so that
+// the workgroups that start late are short.  False: there is none.
+template <int NT>
+__device__ static inline bool packed_span(const LinParams& p, int rows, int at, int* lds, int& n, int& seg) {
+  const int tid = threadIdx.x;
+  int* found = lds + SORTED;
+  if (tid == 0) found[0] = -1;
+  auto len_of = [&](int i) {
+    const int b = min(max(p.cu[i], 0), p.T);
+    return min(max(p.cu[i + 1], b), p.T) - b;
+  };
+  if (p.B <= SORTED) {
+    for (int i = tid; i < p.B; i += NT) lds[i] = len_of(i);
+    __syncthreads();
+    for (int i = tid; i < p.B; i += NT) {
+      // the last segment is a short one, unless the length divides evenly
+      const int len = lds[i], whole = len / rows, rest = len - whole * rows;
+      const bool has_rest = rest > 0 || len == 0;
+      int before = 0, all = 0, longer = 0;
+      for (int j = 0; j < p.B; ++j) {
+        const int l = lds[j], wj = l / rows, rj = l - wj * rows;
+        all += wj;
+        before += j < i ? wj : 0;
+        longer += (rj > 0 || l == 0) && (rj > rest || (rj == rest && j < i));
+      }
+      const int s = at < all ? at - before : (has_rest && at - all == longer ? whole : -1);
+      if (s >= 0 && (at >= all || s < whole)) {
+        found[0] = i;
+        found[1] = s;
+      }
+    }
+  } else {  // too many to be sorted: sequence i has places floor(begin / rows) + i and on
+    __syncthreads();
+    for (int i = tid; i < p.B; i += NT) {
+      const int first = min(max(p.cu[i], 0), p.T) / rows + i, count = max(1, (len_of(i) + rows - 1) / rows);
+      if (at >= first && at < first + count) {
+        found[0] = i;
+        found[1] = at - first;
+      }
+    }
+  }
+  __syncthreads();
+  n = found[0];
+  seg = found[1];
+  __syncthreads();
+  return n >= 0;
+}
+
+// PASS 0: outputs (and end states); PASS 1: the end states of the segments
+// that others follow, each from zero (a sequence's first from S0).
+template <typename TI, int DX, int DZ, int PASS>
+__global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT)) void linear_kernel(const LinParams p) {
+  using K = LK<TI, DX, DZ, PASS>;
+  constexpr int C = K::C;
+  __shared__ __attribute__((aligned(16))) char lds[K::LDS];
+  __shared__ double sPow[C + 1];
+  static_assert(K::LDS >= (SORTED + 2) * 4, "the sequences' lengths pass through the same memory");
+
+  const int tid = threadIdx.x;
+  // Consecutive workgroups go to the XCDs in turn: each XCD has every eighth
+  // chain, and the roles of a chain, which read the same rows, are neighbours
+  // on one.
+  const int k = blockIdx.x >> 3;
+  const int chain = k / p.nrole * 8 + (blockIdx.x & 7);
+  Span sp;
+  sp.ri = k % p.nrole;
+  if (chain >= p.nslots * p.H) return;
+  const int place = chain / p.H;
+  sp.h = chain % p.H;
+  long row0;
+  if (p.cu) {
+    const int rows = p.segc ? p.segc * C : p.T + 1;
+    if (!packed_span<K::NT>(p, rows, place, reinterpret_cast<int*>(lds), sp.n, sp.seg)) return;
+    const int b = min(max(p.cu[sp.n], 0), p.T), e = min(max(p.cu[sp.n + 1], b), p.T);
+    row0 = b;
+    sp.len = e - b;
+    sp.slot = b / rows + sp.n + sp.seg;
+  } else {
+    sp.n = place / p.nseg;
+    sp.seg = place % p.nseg;
+    row0 = (long)sp.n * p.T;
+    sp.len = p.T;
+    sp.slot = place;
+  }
+  sp.th0 = row0 * p.H + sp.h;
+  sp.nch = (sp.len + C - 1) / C;
+  sp.c0 = sp.seg * p.segc;
+  sp.c1 = p.segc ? min(sp.nch, sp.c0 + p.segc) : sp.nch;
+  if (sp.seg > 0 && sp.c0 >= sp.nch) return;
+  const float gh = p.g[sp.h];
+  if constexpr (PASS == 1) {
+    if (sp.c1 >= sp.nch) return;  // nothing follows
+    const double nats = -(double)gh * C;
+    if (nats * (sp.c1 - sp.c0) > FORGOTTEN) sp.c0 = max(sp.c0, sp.c1 - 1 - (int)(FORGOTTEN / nats));
+  }
+  if (tid <= C) sPow[tid] = pow_of(gh, tid);
+  __syncthreads();
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (w < K::NW) compute<TI, DX, DZ, PASS>(p, sp, gh, w, lds, sPow);
+  else copy_chunks<TI, DX, DZ, PASS>(p, sp, lds);
 }
 
 // ------------------------------------------------------------------- host --
 
-// Where a batch has fewer workgroups than the device has compute units, its
-// sequences are cut into segments whose states a first launch forms.
-constexpr int CUS = 256;      // of an MI355X
-constexpr int SEG_MIN = 8;    // chunks a segment has at least
+constexpr int CUS = 256;    // of an MI355X
+constexpr int SEG_MIN = 4;  // chunks a segment has at least
 
-int segment_chunks(int B, int T, int H, int dz, int roles) {
-  const long items = (long)B * H * (dz / ZT) * roles;
-  const int nch = (int)(((long)T + C - 1) / C);
-  if (items <= 0 || items >= CUS || nch < 2 * SEG_MIN) return 0;
-  const int want = (int)std::min<long>((2 * CUS + items - 1) / items, nch / SEG_MIN);
-  return want > 1 ? (nch + want - 1) / want : 0;
+int chunk_rows(int dtype) { return dtype == GDN_BF16 ? 64 : 32; }
+
+// Workgroups of a role of dx x dz that a CU holds (LK::NBUF).
+int residents(int dx, int dz, int dtype) {
+  const int e = dtype == GDN_BF16 ? 2 : 4, slot = chunk_rows(dtype) * (2 * dx + dz) * e, more = 12 * 1024;
+  return 2 * slot + more > 79 * 1024 ? 1 : (3 * slot + more > 53 * 1024 ? 2 : 3);
 }
 
-long segment_slots(int B, int T, bool packed, int segc) {
+// Chunks of a segment, or 0: a sequence is cut where a batch has fewer
+// chains than the device holds workgroups.  What a cut costs is a first
+// launch over y and z, some 0.6 of the second's time a chunk; what it brings
+// is shorter rounds of workgroups.
+int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
+  const long rows = chunk_rows(dtype), chains = (long)B * H * roles, room = (long)CUS * residents(dx, dz, dtype);
+  if (chains <= 0) return 0;
+  if (packed) {
+    // lengths are not known here: no segment is longer than an even share
+    const long all = ((long)T + rows - 1) / rows;
+    const long share = std::max<long>(SEG_MIN, (all * H * roles + room - 1) / room);
+    return share < all ? (int)share : 0;
+  }
+  const long nch = ((long)T + rows - 1) / rows;
+  long best = 0, least = 0;
+  for (long n = 1; n <= 32 && (n == 1 || nch / n >= SEG_MIN); ++n) {
+    const long segc = (nch + n - 1) / n, segs = (nch + segc - 1) / segc;
+    long cost = 10 * ((chains * segs + room - 1) / room) * (segc + 1);
+    if (n > 1) cost += 6 * ((chains * (segs - 1) + room - 1) / room) * (segc + 1) + 20;
+    if (n == 1 || cost < least) {
+      least = cost;
+      best = n == 1 ? 0 : segc;
+    }
+  }
+  return (int)best;
+}
+
+long segment_slots(int B, int T, bool packed, int segc, int dtype) {
   if (!segc) return B;
-  if (packed) return T / ((long)segc * C) + B;
-  return (long)B * ((((long)T + C - 1) / C + segc - 1) / segc);
+  const long rows = (long)segc * chunk_rows(dtype);
+  return packed ? T / rows + B : B * (((long)T + rows - 1) / rows);
 }
 
-template <typename TI, int DX>
-int launch_dx(LinParams p, hipStream_t s) {
-  const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc);
-  p.nslot = p.segc && !p.cu ? (int)(slots / p.B) : 1;
-  const long wgs = slots * p.H * p.nrole * p.tiles;
-  if (wgs <= 0) return GDN_OK;
-  if (wgs >= 1L << 23) return GDN_ERR_INVALID_ARG;
-  const dim3 grid((unsigned)wgs), block(64 * (NWC + 1));
+template <typename TI, int DX, int DZ>
+int launch_kernels(const LinParams& p, long wgs, hipStream_t s) {
   if (p.segc) {
-    hipLaunchKernelGGL((linear_kernel<TI, DX, 1>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 1>), dim3((unsigned)wgs), dim3(LK<TI, DX, DZ, 1>::NT), 0, s, p);
     if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
   }
-  hipLaunchKernelGGL((linear_kernel<TI, DX, 0>), grid, block, 0, s, p);
+  hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 0>), dim3((unsigned)wgs), dim3(LK<TI, DX, DZ, 0>::NT), 0, s, p);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-int launch(const LinParams& p, int dx, int dtype, hipStream_t s) {
+template <typename TI, int DX>
+int launch_dz(const LinParams& p, int dz, long wgs, hipStream_t s) {
+  switch (dz) {
+    case 32: return launch_kernels<TI, DX, 32>(p, wgs, s);
+    case 64: return launch_kernels<TI, DX, 64>(p, wgs, s);
+    default: return launch_kernels<TI, DX, 128>(p, wgs, s);
+  }
+}
+
+int launch(LinParams p, int dx, int dz, int dtype, hipStream_t s) {
+  const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc, dtype);
+  const long wgs = (slots * p.H + 7) / 8 * 8 * p.nrole;
+  if (wgs >= 1L << 22) return GDN_ERR_INVALID_ARG;
+  p.nslots = (int)slots;
+  p.nseg = p.segc && !p.cu ? (int)(slots / p.B) : 1;
   const bool b16 = dtype == GDN_BF16;
   switch (dx) {
-    case 32: return b16 ? launch_dx<__bf16, 32>(p, s) : launch_dx<float, 32>(p, s);
-    case 64: return b16 ? launch_dx<__bf16, 64>(p, s) : launch_dx<float, 64>(p, s);
-    default: return b16 ? launch_dx<__bf16, 128>(p, s) : launch_dx<float, 128>(p, s);
+    case 32: return b16 ? launch_dz<__bf16, 32>(p, dz, wgs, s) : launch_dz<float, 32>(p, dz, wgs, s);
+    case 64: return b16 ? launch_dz<__bf16, 64>(p, dz, wgs, s) : launch_dz<float, 64>(p, dz, wgs, s);
+    default: return b16 ? launch_dz<__bf16, 128>(p, dz, wgs, s) : launch_dz<float, 128>(p, dz, wgs, s);
   }
 }
 
@@ -540,10 +627,10 @@ struct Plan {
 };
 
 // One launch of `roles` roles of states dx x dz.
-Plan plan(int B, int T, int H, int dx, int dz, int roles, bool packed) {
-  const int segc = segment_chunks(B, T, H, dz, roles);
+Plan plan(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
+  const int segc = segment_chunks(B, T, H, dx, dz, roles, packed, dtype);
   if (!segc) return {0, 0};
-  return {segc, segment_slots(B, T, packed, segc) * H * roles * dx * dz * 4LL};
+  return {segc, segment_slots(B, T, packed, segc, dtype) * H * roles * dx * dz * 4LL};
 }
 
 }  // namespace
@@ -552,9 +639,9 @@ extern "C" long long gdn_linear_workspace_size(int B, int T, int H, int dk, int 
                                                int backward) {
   const int rc = check_sizes(B, T, H, dk, dv, packed != 0, dtype);
   if (rc != GDN_OK) return rc;
-  if (!backward) return plan(B, T, H, dk, dv, 1, packed != 0).bytes;
-  if (dk == dv) return plan(B, T, H, dk, dv, 3, packed != 0).bytes;
-  return plan(B, T, H, dv, dk, 2, packed != 0).bytes + plan(B, T, H, dk, dv, 1, packed != 0).bytes;
+  if (!backward) return plan(B, T, H, dk, dv, 1, packed != 0, dtype).bytes;
+  if (dk == dv) return plan(B, T, H, dk, dv, 3, packed != 0, dtype).bytes;
+  return plan(B, T, H, dv, dk, 2, packed != 0, dtype).bytes + plan(B, T, H, dk, dv, 1, packed != 0, dtype).bytes;
 }
 
 extern "C" int gdn_linear_fwd(const void* q, const void* k, const void* v, const float* g, const float* h0,
@@ -564,7 +651,7 @@ extern "C" int gdn_linear_fwd(const void* q, const void* k, const void* v, const
   const int rc = check_sizes(B, T, H, dk, dv, packed, dtype);
   if (rc != GDN_OK) return rc;
   if (B > 0 && (!g || !hT || (T > 0 && (!q || !k || !v || !out)))) return GDN_ERR_INVALID_ARG;
-  Plan pl = plan(B, T, H, dk, dv, 1, packed);
+  Plan pl = plan(B, T, H, dk, dv, 1, packed, dtype);
   if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return GDN_ERR_INVALID_ARG;
   if (misaligned({q, k, v, h0, out, hT, workspace}, 16) || misaligned({g, cu_seqlens}, 4)) return GDN_ERR_INVALID_ARG;
   const long long th = (packed ? 1LL : B) * T * H, e = dtype == GDN_BF16 ? 2 : 4, state = (long long)B * H * dk * dv * 4;
@@ -583,9 +670,8 @@ extern "C" int gdn_linear_fwd(const void* q, const void* k, const void* v, const
   p.T = T;
   p.H = H;
   p.nrole = 1;
-  p.tiles = dv / ZT;
   p.segc = pl.segc;
-  return launch(p, dk, dtype, static_cast<hipStream_t>(stream));
+  return launch(p, dk, dv, dtype, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int gdn_linear_bwd(const void* q, const void* k, const void* v, const float* g, const float* h0,
@@ -625,23 +711,20 @@ extern "C" int gdn_linear_bwd(const void* q, const void* k, const void* v, const
     p.role[1] = rk;
     p.role[2] = rv;
     p.nrole = 3;
-    p.tiles = dv_ / ZT;
-    p.segc = plan(B, T, H, dk_, dv_, 3, packed).segc;
-    return launch(p, dk_, dtype, s);
+    p.segc = plan(B, T, H, dk_, dv_, 3, packed, dtype).segc;
+    return launch(p, dk_, dv_, dtype, s);
   }
-  const Plan first = plan(B, T, H, dv_, dk_, 2, packed);
+  const Plan first = plan(B, T, H, dv_, dk_, 2, packed, dtype);
   const bool fits = dk_ != dv_;  // the workspace of equal widths is that of one launch: leave these two uncut
   p.role[0] = rq;
   p.role[1] = rk;
   p.nrole = 2;
-  p.tiles = dk_ / ZT;
   p.segc = fits ? first.segc : 0;
-  const int rc2 = launch(p, dv_, dtype, s);
+  const int rc2 = launch(p, dv_, dk_, dtype, s);
   if (rc2 != GDN_OK) return rc2;
   p.role[0] = rv;
   p.nrole = 1;
-  p.tiles = dv_ / ZT;
-  p.segc = fits && !in_place ? plan(B, T, H, dk_, dv_, 1, packed).segc : 0;
+  p.segc = fits && !in_place ? plan(B, T, H, dk_, dv_, 1, packed, dtype).segc : 0;
   p.ws = reinterpret_cast<f32x4*>(static_cast<char*>(workspace) + (fits ? first.bytes : 0));
-  return launch(p, dk_, dtype, s);
+  return launch(p, dk_, dv_, dtype, s);
 }
