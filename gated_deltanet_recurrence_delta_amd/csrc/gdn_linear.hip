@@ -70,17 +70,20 @@ struct LK {
   static constexpr bool B16 = sizeof(TI) == 2;
   static constexpr int ES = sizeof(TI), SLAB = Mma<TI>::SLAB, E = Mma<TI>::E;
   static constexpr int C = B16 ? 64 : 32, NB = C / 16;         // rows of a chunk, 16-row blocks
-  static constexpr int NW = DZ / 16, NT = 64 * (NW + 1);       // computing waves, threads
+  static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
   static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
   static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
-  // LDS: NBUF chunks of (x,) y and z, the scores, their decays.  Two
+  // LDS: NBUF chunks of (x,) y and z, the scores, and their decays.  Two
   // workgroups on a CU where that leaves two chunks each, else three chunks.
-  static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, XB = PASS == 0 ? YB : 0, SB = XB + YB + ZB;
+  static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, AT_Y = PASS == 0 ? YB : 0, AT_Z = AT_Y + YB, SB = AT_Z + ZB;
   static constexpr int PB = PASS == 0 ? NB * NJS * 1024 : 0, DB = PASS == 0 ? NB * 1024 : 0;
-  static constexpr int NBUF = 3 * SB + PB + DB <= 79 * 1024 || 2 * SB + PB + DB > 79 * 1024 ? 3 : 2;
-  static constexpr int LDS = NBUF * SB + PB + DB;
-  static constexpr int X_INS = XB / 1024, Y_INS = YB / 1024, Z_INS = ZB / 1024, INS = X_INS + Y_INS + Z_INS;
-  static_assert((NBUF - 2) * INS < 64, "copies in flight are counted in six bits");
+  static constexpr int NBUF = 3 * SB + PB + DB <= 78 * 1024 || 2 * SB + PB + DB > 78 * 1024 ? 3 : 2;
+  static constexpr int AT_P = NBUF * SB, AT_D = AT_P + PB, LDS = AT_D + DB;
+  static constexpr int Y_INS = YB / 1024, Z_INS = ZB / 1024;  // copies of 1 KB
+  // A wave's copies a chunk, at least, and its stores.
+  static constexpr int COPIES = (Y_INS >= NW ? (PASS == 0 ? 2 : 1) * Y_INS / NW : 0) + Z_INS / NW;
+  static constexpr int STORES = PASS == 0 ? NB : 0;
+  static_assert((NBUF - 2) * COPIES + STORES < 64, "operations in flight are counted in six bits");
   // In 16-bit storage a transposing read takes four neighbouring values of a
   // row, half a granule.  The halves alternate from granule to granule, so
   // that a read covers all banks: accumulator row m = 4 q + e of tile t of a
@@ -98,26 +101,27 @@ struct LK {
   }
 };
 
-// exp(n g), and what its rounding to 32 bits leaves: a constant factor's
-// rounding would add up over the chunks, always to the same side.
-struct Pow {
-  float hi, lo;
+// A state's decay over n rows.  A constant factor's rounding would add up
+// over the chunks, always to the same side: near one it is applied as
+// m + (a^n - 1) m, whose rounding goes either way.
+struct Decay {
+  float f;
+  bool near_one;
 };
-__device__ static inline Pow split_pow(double d) {
-  const float hi = (float)d;
-  return {hi, d > 1e-30 && d < 1e30 ? (float)(d - (double)hi) : 0.f};
-}
+__device__ static inline Decay decay_of(double d) { return {(float)(d > 0.5 ? d - 1.0 : d), d > 0.5}; }
 __device__ static inline double pow_of(float g, long n) { return n == 0 ? 1.0 : exp((double)g * (double)n); }
-__device__ static inline f32x4 decayed(f32x4 m, Pow a) {
-  f32x4 r;
+template <bool NEAR_ONE, int N>
+__device__ static inline void apply(const float f, f32x4 (&m)[N]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] = __builtin_fmaf(a.hi, m[e], a.lo * m[e]);
-  return r;
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[u][e] = NEAR_ONE ? __builtin_fmaf(m[u][e], f, m[u][e]) : m[u][e] * f;
 }
 
-template <typename V>
-__device__ static inline V buf_load16(__amdgpu_buffer_rsrc_t r, int off) {
-  return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+// What four values' rounding to bf16 (two packed pairs) left of them, exactly.
+__device__ static inline f32x4 left_over(f32x4 x, u32x2 t) {
+  return f32x4{x[0] - __uint_as_float(t[0] << 16), x[1] - __uint_as_float(t[0] & 0xffff0000u),
+               x[2] - __uint_as_float(t[1] << 16), x[3] - __uint_as_float(t[1] & 0xffff0000u)};
 }
 
 // Where a workgroup's chain and segment lie.
@@ -130,19 +134,86 @@ struct Span {
 // end state: e^-60 of their own share, far below what 32 bits can add up.
 constexpr double FORGOTTEN = 60.0;
 
-// A computing wave's part.
+// 16 bytes a lane from the buffer to LDS, from `at` on.  From assembly: the
+// copy writes LDS only, and as a builtin it would make the compiler wait for
+// all of a wave's copies before each of its own LDS reads.  The waits stand
+// before the barriers that hand a chunk over.  (The wait states are for a
+// descriptor or an address that a vector instruction has just put into scalar
+// registers: the compiler does not look into the assembly.)
+__device__ static inline void lds_copy(unsigned at, int off, __amdgpu_buffer_rsrc_t r) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(at), "v"(off), "s"(r));
+#endif
+}
+
+// A wave's share of the copies of one stream's chunks to LDS: INS copies a
+// chunk among NW waves, rows of G16 granules.
+template <int INS, int NW, int G16>
+struct Copier {
+  static constexpr int MINE = (INS + NW - 1) / NW;
+  static_assert(INS % NW == 0 || INS < NW, "even shares");
+  __amdgpu_buffer_rsrc_t rsrc;
+  unsigned off[MINE], step, at;
+  bool any;
+
+  // `base`: the sequence's first row; `place(row, granule)`: where a granule of a row lies in the buffer's row
+  template <typename F>
+  __device__ inline Copier(const char* base, int stride, int len, int rev, unsigned first, int rows, int w,
+                           const char* lds, F place) {
+    const int lane = threadIdx.x & 63;
+    rsrc = make_rsrc(base, (long)(len - 1) * stride + G16 * 16);
+    any = INS >= NW || w < INS;
+    at = (unsigned)(uintptr_t)(const __attribute__((address_space(3))) char*)lds + w * MINE * 1024;
+    step = (unsigned)(rev ? -rows : rows) * (unsigned)stride;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      const int G = (w * MINE + k) * 64 + lane, r = G / G16;
+      // Rows outside the sequence lie outside the descriptor (a negative
+      // offset wraps far behind it) and read as zeros.
+      off[k] = (rev ? (unsigned)(len - 1) - first - r : first + r) * (unsigned)stride + 16 * place(r, G % G16);
+    }
+  }
+  // The next chunk to `shift` bytes behind the first buffer; without `in`,
+  // zeros, so that the loop over the chunks has no branch for its last one.
+  __device__ inline void issue(int shift, bool in) {
+    if (INS >= NW || any) {
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        lds_copy(at + shift + k * 1024, in ? (int)off[k] : -16, rsrc);
+        off[k] += step;
+      }
+    }
+  }
+};
+
+// A wave's part.
 template <typename TI, int DX, int DZ, int PASS>
 __device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds,
-                                      const double* sPow) {
+                                      const double* sPow, const float* sIn) {
   using K = LK<TI, DX, DZ, PASS>;
   using Frag = typename K::Frag;
   constexpr int C = K::C;
   const Role& role = p.role[sp.ri];
   const int lane = threadIdx.x & 63, m16 = lane & 15, q4 = lane >> 4;
   const int H = p.H, rev = role.reverse, len = sp.len;
-  char* const sP = lds + K::NBUF * K::SB;
-  char* const sD = sP + K::PB;
+  char* const sP = lds + K::AT_P;
+  char* const sD = lds + K::AT_D;
   const int z_at = 16 * w + m16;  // the lane's state column
+  const int x_stride = H * DX * K::ES, z_stride = H * DZ * K::ES;
+  const unsigned row0 = (unsigned)sp.c0 * C;
+  auto place_y = [](int r, int g) { return g ^ K::swz_y(r); };
+  auto place_z = [](int r, int g) { return g ^ K::swz_z(r); };
+  const long x0 = sp.th0 * DX * K::ES;
+  Copier<K::Y_INS, K::NW, K::GR> cx(role.x + x0, x_stride, len, rev, row0, C, w, lds, place_y);
+  Copier<K::Y_INS, K::NW, K::GR> cy(role.y + x0, x_stride, len, rev, row0, C, w, lds + K::AT_Y, place_y);
+  Copier<K::Z_INS, K::NW, K::ZGR> cz(role.z + sp.th0 * DZ * K::ES, z_stride, len, rev, row0, C, w, lds + K::AT_Z, place_z);
+  auto issue = [&](int slot, bool in) {
+    if constexpr (PASS == 0) cx.issue(slot * K::SB, in);
+    cy.issue(slot * K::SB, in);
+    cz.issue(slot * K::SB, in);
+  };
+#pragma unroll
+  for (int i = 0; i < K::NBUF - 1; ++i) issue(i, sp.c0 + i < sp.c1);
 
   // The state: tile u has x rows x_at(u) and on.
   f32x4 M[K::NU];
@@ -166,34 +237,23 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       }
     }
   } else if (PASS == 0) {
-    const Pow a = split_pow(pow_of(gh, (long)p.segc * C));
+    const Decay a = decay_of(pow_of(gh, (long)p.segc * C));
     const double nats = -(double)gh * p.segc * C;
     const int first = nats * sp.seg > FORGOTTEN ? max(sp.slot - sp.seg, sp.slot - 1 - (int)(FORGOTTEN / nats))
                                                 : sp.slot - sp.seg;
     for (int s = first; s < sp.slot; ++s) {
       const f32x4* src = ws_at(s);
+      if (a.near_one) apply<true>(a.f, M);
+      else apply<false>(a.f, M);
 #pragma unroll
-      for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], a) + src[u * 64];
+      for (int u = 0; u < K::NU; ++u) M[u] += src[u * 64];
     }
   }
 
-  // Powers of the decay: the state's at output row i = 16 ib + m16, the
-  // inputs' at row j = 16 jb + 4 q4 + e.  Backwards the state's are one lower
-  // and the inputs' one higher.
-  f32x4 Wj[K::NB];
+  // The state's power of the decay at output row i = 16 ib + m16; backwards
+  // one lower, as the inputs' at row j are one higher.
   float gam[K::NB];
-  auto input_powers = [&](int rows) {
-#pragma unroll
-    for (int jb = 0; jb < K::NB; ++jb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = rows - 1 - (16 * jb + 4 * q4 + e) + rev;
-        Wj[jb][e] = d >= 0 ? (float)sPow[d] : 0.f;
-      }
-  };
-  input_powers(C);
-  Pow step = split_pow(sPow[C]);
-  const int z_stride = H * DZ * K::ES;
+  const Decay step = decay_of(sPow[C]);
   const __amdgpu_buffer_rsrc_t ro = make_rsrc(role.out + sp.th0 * DZ * K::ES, (long)(len - 1) * z_stride + DZ * K::ES);
   unsigned o_off = 0;
   const unsigned o_step = (unsigned)(rev ? -C : C) * (unsigned)z_stride;
@@ -216,14 +276,17 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
     }
     for (int f = w; f < K::NB * K::NJS; f += K::NW) lds_st(sP, (f * 64 + lane) * 16, f32x4{0.f, 0.f, 0.f, 0.f});
   }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::COPIES));  // the first chunk
   lds_barrier();
 
   const int tr_r = 4 * q4 + (m16 >> 2), tr_g = m16 & 3;
   int slot = 0;
+  auto walk = [&](auto near_one) {
   for (int c = sp.c0; c < sp.c1; ++c) {
     const char* bX = lds + slot * K::SB;
-    const char* bY = bX + K::XB;
-    const char* bZ = bY + K::YB;
+    const char* bY = bX + K::AT_Y;
+    const char* bZ = bX + K::AT_Z;
+    issue(slot == 0 ? K::NBUF - 1 : slot - 1, c + K::NBUF - 1 < sp.c1);
     slot = slot + 1 == K::NBUF ? 0 : slot + 1;
 
     // z columns as fragments over the rows (for two 16-row blocks: rows 4 q4
@@ -282,8 +345,11 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
           const int g = (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16;
           O[ib] = Mma<TI>::mma(Mf[s], lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + g), O[ib]);
         }
-        O[ib] *= gam[ib];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[ib][e] *= gam[ib];
       }
+#pragma unroll
+      for (int ib = 0; ib < K::NB; ++ib) settle(O[ib]);  // before the barrier, not behind it
       lds_barrier();  // the scores are there
       // the chunk's own part
 #pragma unroll
@@ -300,14 +366,13 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       o_off += o_step;
     }
 
-    // the state: decayed rows y z^T; in 16-bit storage the decayed z are
-    // taken as three terms, their 24 bits in full
-    if (len - c * C < C) {  // the last chunk
-      input_powers(len - c * C);
-      step = split_pow(sPow[len - c * C]);
-    }
-#pragma unroll
-    for (int u = 0; u < K::NU; ++u) M[u] = decayed(M[u], step);
+    // the state: decayed, and the chunk's y z^T, decayed z in 16-bit storage
+    // as three terms, their 24 bits in full
+    const int rows = min(C, len - c * C);
+    // a shorter last chunk: its decay is no further from one, or comes once only
+    const float last = (float)(decltype(near_one)::value ? sPow[rows] - 1.0 : sPow[rows]);
+    apply<decltype(near_one)::value != 0>(rows < C ? last : step.f, M);
+    const float* in_pow = sIn + C - (rows - 1 + rev) + 4 * q4;  // of row 4 q4; rows behind the last have zeros
 #pragma unroll
     for (int js = 0; js < K::NJS; ++js) {
       constexpr int TERMS = K::B16 ? 3 : 1;
@@ -316,44 +381,60 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
         f32x4 a, b;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          a[e] = (float)Zf[js][e] * Wj[2 * js][e];
-          b[e] = (float)Zf[js][4 + e] * Wj[2 * js + 1][e];
+          a[e] = (float)Zf[js][e] * in_pow[32 * js + e];
+          b[e] = (float)Zf[js][4 + e] * in_pow[32 * js + 16 + e];
         }
 #pragma unroll
         for (int i = 0; i < TERMS; ++i) {
-          zt[i] = Mma<TI>::from_acc(a, b);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] -= (float)zt[i][e];
-            b[e] -= (float)zt[i][4 + e];
+          const u32x2 ta = __builtin_bit_cast(u32x2, cvt4(a)), tb = __builtin_bit_cast(u32x2, cvt4(b));
+          zt[i] = __builtin_bit_cast(Frag, u32x4{ta[0], ta[1], tb[0], tb[1]});
+          if (i + 1 < TERMS) {
+            a = left_over(a, ta);
+            b = left_over(b, tb);
           }
         }
       } else {
-        zt[0] = Zf[js] * Wj[js];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zt[0][e] = Zf[js][e] * in_pow[16 * js + e];
       }
+      constexpr int UB = K::NU < 4 ? K::NU : 4;  // tiles at a time: independent products one behind another
 #pragma unroll
-      for (int u = 0; u < K::NU; ++u) {
-        Frag y;
-        if constexpr (K::B16) {
-          const char* at = bY + tr_r * (K::GR * 16) + (((4 * (u / 2) + tr_g) ^ K::swz_y(tr_r)) * 16) +
-                           2 * K::half_of(u & 1, tr_g);
-          const bf16x4 lo = lds_read_tr(at, 32 * js * (K::GR * 16));
-          const bf16x4 hi = lds_read_tr(at, (32 * js + 16) * (K::GR * 16));
-          y = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-          const int x = u * 16 + m16;
+      for (int u0 = 0; u0 < K::NU; u0 += UB) {
+        Frag y[UB];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 16 * js + 4 * q4 + e;
-            y[e] = lds_ld<float>(bY, r * (K::GR * 16) + (((x >> 2) ^ K::swz_y(r)) * 16) + (x & 3) * 4);
+        for (int v = 0; v < UB; ++v) {
+          const int u = u0 + v;
+          if constexpr (K::B16) {
+            const char* at = bY + tr_r * (K::GR * 16) + (((4 * (u / 2) + tr_g) ^ K::swz_y(tr_r)) * 16) +
+                             2 * K::half_of(u & 1, tr_g);
+            const bf16x4 lo = lds_read_tr(at, 32 * js * (K::GR * 16));
+            const bf16x4 hi = lds_read_tr(at, (32 * js + 16) * (K::GR * 16));
+            y[v] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          } else {
+            const int x = u * 16 + m16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 16 * js + 4 * q4 + e;
+              y[v][e] = lds_ld<float>(bY, r * (K::GR * 16) + (((x >> 2) ^ K::swz_y(r)) * 16) + (x & 3) * 4);
+            }
           }
         }
 #pragma unroll
-        for (int i = TERMS - 1; i >= 0; --i) M[u] = Mma<TI>::mma(y, zt[i], M[u]);
+        for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+          for (int v = 0; v < UB; ++v) M[u0 + v] = Mma<TI>::mma(y[v], zt[i], M[u0 + v]);
       }
     }
+    // The next chunk has arrived: behind its copies are, at least, those of
+    // the chunks after it and this chunk's stores.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::COPIES + K::STORES));
     lds_barrier();
   }
+  };
+  // One loop for each kind of decay: a choice inside it would cost a copy of the state a chunk.
+  if (step.near_one) walk(IC<1>{});
+  else walk(IC<0>{});
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // no copy outlives the workgroup's LDS
 
   if constexpr (PASS == 1) {
     f32x4* dst = ws_at(sp.slot);
@@ -365,63 +446,6 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
     for (int u = 0; u < K::NU; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sT[(x_at(u) + e) * DZ + z_at] = M[u][e];
-  }
-}
-
-// The copying wave's part: chunks of x, y and z to LDS, NBUF - 1 ahead.
-template <typename TI, int DX, int DZ, int PASS>
-__device__ static inline void copy_chunks(const LinParams& p, const Span& sp, char* lds) {
-  using K = LK<TI, DX, DZ, PASS>;
-  constexpr int C = K::C;
-  const Role& role = p.role[sp.ri];
-  const int lane = threadIdx.x & 63, rev = role.reverse, len = sp.len;
-  const int y_stride = p.H * DX * K::ES, z_stride = p.H * DZ * K::ES;
-  const long y_bytes = (long)(len - 1) * y_stride + DX * K::ES;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(role.x + sp.th0 * DX * K::ES, y_bytes);
-  const __amdgpu_buffer_rsrc_t ry = make_rsrc(role.y + sp.th0 * DX * K::ES, y_bytes);
-  const __amdgpu_buffer_rsrc_t rz =
-      make_rsrc(role.z + sp.th0 * DZ * K::ES, (long)(len - 1) * z_stride + DZ * K::ES);
-  int y_off[K::Y_INS], z_off[K::Z_INS];
-#pragma unroll
-  for (int i = 0; i < K::Y_INS; ++i) {
-    const int G = i * 64 + lane, r = G / K::GR;
-    y_off[i] = (rev ? -r : r) * y_stride + ((G % K::GR) ^ K::swz_y(r)) * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < K::Z_INS; ++i) {
-    const int G = i * 64 + lane, r = G / K::ZGR;
-    z_off[i] = (rev ? -r : r) * z_stride + ((G % K::ZGR) ^ K::swz_z(r)) * 16;
-  }
-  // Rows outside the sequence lie outside the descriptors (a negative offset
-  // wraps far behind them) and read as zeros; so do the chunks behind the
-  // last, asked for to keep the count of copies even.
-  int slot = 0;
-  auto issue = [&](int c) {
-    char* d = lds + slot * K::SB;
-    slot = slot + 1 == K::NBUF ? 0 : slot + 1;
-    const unsigned at = rev ? (unsigned)(len - 1) - (unsigned)c * C : (unsigned)c * C;
-    const unsigned ya = at * (unsigned)y_stride, za = at * (unsigned)z_stride;
-    const bool in = c < sp.c1;
-#pragma unroll
-    for (int i = 0; i < K::X_INS; ++i) copy_to_lds(rx, d + i * 1024, in ? (int)(ya + (unsigned)y_off[i]) : -16);
-    d += K::XB;
-#pragma unroll
-    for (int i = 0; i < K::Y_INS; ++i) copy_to_lds(ry, d + i * 1024, in ? (int)(ya + (unsigned)y_off[i]) : -16);
-    d += K::YB;
-#pragma unroll
-    for (int i = 0; i < K::Z_INS; ++i) copy_to_lds(rz, d + i * 1024, in ? (int)(za + (unsigned)z_off[i]) : -16);
-  };
-  if (sp.c0 < sp.c1) {
-#pragma unroll
-    for (int i = 0; i < K::NBUF - 1; ++i) issue(sp.c0 + i);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::INS));
-  }
-  lds_barrier();
-  for (int c = sp.c0; c < sp.c1; ++c) {
-    issue(c + K::NBUF - 1);
-    if constexpr (PASS == 0) lds_barrier();  // the scores are there
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::INS));
-    lds_barrier();
   }
 }
 
@@ -470,8 +494,8 @@ __device__ static inline bool packed_span(const LinParams& p, int rows, int at, 
     }
   }
   __syncthreads();
-  n = found[0];
-  seg = found[1];
+  n = __builtin_amdgcn_readfirstlane(found[0]);  // one for all: what follows from it stays in scalar registers
+  seg = __builtin_amdgcn_readfirstlane(found[1]);
   __syncthreads();
   return n >= 0;
 }
@@ -479,11 +503,13 @@ __device__ static inline bool packed_span(const LinParams& p, int rows, int at, 
 // PASS 0: outputs (and end states); PASS 1: the end states of the segments
 // that others follow, each from zero (a sequence's first from S0).
 template <typename TI, int DX, int DZ, int PASS>
-__global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT)) void linear_kernel(const LinParams p) {
+__global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(const LinParams p) {
   using K = LK<TI, DX, DZ, PASS>;
   constexpr int C = K::C;
   __shared__ __attribute__((aligned(16))) char lds[K::LDS];
   __shared__ double sPow[C + 1];
+  __shared__ float sIn[2 * C];  // the decay's powers from C down to 0, then zeros
+  static_assert(K::NT >= 2 * C, "a thread for each");
   static_assert(K::LDS >= (SORTED + 2) * 4, "the sequences' lengths pass through the same memory");
 
   const int tid = threadIdx.x;
@@ -523,11 +549,15 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT)) void linear_kernel(cons
     const double nats = -(double)gh * C;
     if (nats * (sp.c1 - sp.c0) > FORGOTTEN) sp.c0 = max(sp.c0, sp.c1 - 1 - (int)(FORGOTTEN / nats));
   }
-  if (tid <= C) sPow[tid] = pow_of(gh, tid);
+  if (tid <= C) {
+    const double a = pow_of(gh, tid);
+    sPow[tid] = a;
+    sIn[C - tid] = (float)a;
+  } else if (tid < 2 * C) {
+    sIn[tid] = 0.f;
+  }
   __syncthreads();
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (w < K::NW) compute<TI, DX, DZ, PASS>(p, sp, gh, w, lds, sPow);
-  else copy_chunks<TI, DX, DZ, PASS>(p, sp, lds);
+  compute<TI, DX, DZ, PASS>(p, sp, gh, __builtin_amdgcn_readfirstlane(tid >> 6), lds, sPow, sIn);
 }
 
 // ------------------------------------------------------------------- host --
@@ -537,10 +567,10 @@ constexpr int SEG_MIN = 4;  // chunks a segment has at least
 
 int chunk_rows(int dtype) { return dtype == GDN_BF16 ? 64 : 32; }
 
-// Workgroups of a role of dx x dz that a CU holds (LK::NBUF).
+// Workgroups of a role of dx x dz that a CU holds: by LDS, and 16 waves.
 int residents(int dx, int dz, int dtype) {
-  const int e = dtype == GDN_BF16 ? 2 : 4, slot = chunk_rows(dtype) * (2 * dx + dz) * e, more = 12 * 1024;
-  return 2 * slot + more > 79 * 1024 ? 1 : (3 * slot + more > 53 * 1024 ? 2 : 3);
+  const int lds = chunk_rows(dtype) * (3 * dx + dz) * (dtype == GDN_BF16 ? 2 : 4) + 13 * 1024;
+  return std::min(160 * 1024 / lds, 16 * 16 / dz);
 }
 
 // Chunks of a segment, or 0: a sequence is cut where a batch has fewer
@@ -548,7 +578,7 @@ int residents(int dx, int dz, int dtype) {
 // launch over y and z, some 0.6 of the second's time a chunk; what it brings
 // is shorter rounds of workgroups.
 int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
-  const long rows = chunk_rows(dtype), chains = (long)B * H * roles, room = (long)CUS * residents(dx, dz, dtype);
+  const long rows = chunk_rows(dtype), chains = (long)B * H * roles, room = CUS;
   if (chains <= 0) return 0;
   if (packed) {
     // lengths are not known here: no segment is longer than an even share
