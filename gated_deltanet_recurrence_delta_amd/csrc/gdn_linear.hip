@@ -69,21 +69,30 @@ struct LK {
   using Frag = typename Mma<TI>::frag;
   static constexpr bool B16 = sizeof(TI) == 2;
   static constexpr int ES = sizeof(TI), SLAB = Mma<TI>::SLAB, E = Mma<TI>::E;
-  static constexpr int C = B16 ? 64 : 32, NB = C / 16;         // rows of a chunk, 16-row blocks
+  // Rows of a chunk, 16-row blocks: the longest that leaves three chunks in
+  // LDS for the largest states, half of that for the others, whose fewer
+  // waves need more workgroups on a CU.
+  static constexpr int C = (DX == 128 && DZ == 128 ? 2 : 1) * (B16 ? 32 : 16), NB = C / 16;
   static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
   static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
   static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
-  // LDS: NBUF chunks of (x,) y and z, the scores, and their decays.  Two
-  // workgroups on a CU where that leaves two chunks each, else three chunks.
+  // LDS: three chunks of (x,) y and z, the scores of two chunks, and decays
+  // of scores.
   static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, AT_Y = PASS == 0 ? YB : 0, AT_Z = AT_Y + YB, SB = AT_Z + ZB;
-  static constexpr int PB = PASS == 0 ? NB * NJS * 1024 : 0, DB = PASS == 0 ? NB * 1024 : 0;
-  static constexpr int NBUF = 3 * SB + PB + DB <= 78 * 1024 || 2 * SB + PB + DB > 78 * 1024 ? 3 : 2;
-  static constexpr int AT_P = NBUF * SB, AT_D = AT_P + PB, LDS = AT_D + DB;
+  static constexpr int NBUF = 3;
+  // Fragments of scores, rows 16 ib and on against SLAB columns from SLAB js on.
+  __host__ __device__ static constexpr int frag_at(int ib, int js) {
+    int n = js;
+    for (int i = 0; i < ib; ++i) n += i / TPS + 1;
+    return n;
+  }
+  static constexpr int NFR = frag_at(NB, 0), PB = PASS == 0 ? NFR * 1024 : 0, DB = PASS == 0 ? 2048 : 0;
+  static constexpr int AT_P = NBUF * SB, AT_D = AT_P + 2 * PB, LDS = AT_D + DB;
   static constexpr int Y_INS = YB / 1024, Z_INS = ZB / 1024;  // copies of 1 KB
   // A wave's copies a chunk, at least, and its stores.
-  static constexpr int COPIES = (Y_INS >= NW ? (PASS == 0 ? 2 : 1) * Y_INS / NW : 0) + Z_INS / NW;
+  static constexpr int COPIES = (Y_INS >= NW ? (PASS == 0 ? 2 : 1) * Y_INS / NW : 0) + (Z_INS >= NW ? Z_INS / NW : 0);
   static constexpr int STORES = PASS == 0 ? NB : 0;
-  static_assert((NBUF - 2) * COPIES + STORES < 64, "operations in flight are counted in six bits");
+  static_assert(COPIES + STORES < 64, "operations in flight are counted in six bits");
   // In 16-bit storage a transposing read takes four neighbouring values of a
   // row, half a granule.  The halves alternate from granule to granule, so
   // that a read covers all banks: accumulator row m = 4 q + e of tile t of a
@@ -263,31 +272,71 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
     for (int ib = 0; ib < K::NB; ++ib) gam[ib] = (float)sPow[16 * ib + m16 + 1 - rev];
     const unsigned i = (unsigned)sp.c0 * C + m16;
     o_off = (rev ? (unsigned)(len - 1) - i : i) * (unsigned)z_stride + (16 * w + 4 * q4) * K::ES;
-    // The decays of a block of scores (row i = 16 ib + m16, column j = 16 jb
-    // + 4 q4 + e), by ib - jb; and the zeros beside the diagonal blocks.
-    for (int d = w; d < K::NB; d += K::NW) {
+    // The decays of a block of scores (row 16 ib + m16, column 16 jb + 4 q4 +
+    // e) on the diagonal and beside it; and the zeros beside diagonal blocks.
+    for (int d = w; d < 2; d += K::NW) {
       f32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = 16 * d + m16 - 4 * q4 - e;
-        v[e] = n >= 0 ? (float)sPow[n] : 0.f;
+        v[e] = n >= 0 ? (float)pow_of(gh, n) : 0.f;
       }
       lds_st(sD, (d * 64 + lane) * 16, v);
     }
-    for (int f = w; f < K::NB * K::NJS; f += K::NW) lds_st(sP, (f * 64 + lane) * 16, f32x4{0.f, 0.f, 0.f, 0.f});
+    for (int f = w; f < 2 * K::NFR; f += K::NW) lds_st(sP, (f * 64 + lane) * 16, f32x4{0.f, 0.f, 0.f, 0.f});
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::COPIES));  // the first chunk
+  const int tr_r = 4 * q4 + (m16 >> 2), tr_g = m16 & 3;
+  const int x_row = m16 * (K::GR * 16);
+  auto x_granule = [&](int s) { return (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16; };
+  // This wave's blocks of a chunk's scores, transposed and masked.
+  auto scores = [&](const char* at_chunk, char* to) {
+    auto block = [&](int ib, int jb) {
+      const char* bX = at_chunk + 16 * ib * (K::GR * 16);
+      const char* bY = at_chunk + K::AT_Y + 16 * jb * (K::GR * 16);
+      f32x4 P = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < K::NS; ++s)
+        P = Mma<TI>::mma(lds_ld<Frag>(bY, x_row + x_granule(s)), lds_ld<Frag>(bX, x_row + x_granule(s)), P);
+      const int d = ib - jb;
+      const f32x4 decay = lds_ld<f32x4>(sD, ((d > 0) * 64 + lane) * 16);
+      const float more = sIn[C - (d > 1 ? 16 * (d - 1) : 0)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) P[e] = P[e] * decay[e] * more;
+      char* at = to + (K::frag_at(ib, jb / K::TPS) * 64 + lane) * 16;
+      if constexpr (K::B16) lds_st(at, 8 * (jb & 1), cvt4(P));
+      else lds_st(at, 0, P);
+    };
+    constexpr int BLOCKS = K::NB * (K::NB + 1) / 2;
+#pragma unroll
+    for (int b0 = 0; b0 < BLOCKS; b0 += K::NW) {
+      const int b = b0 + w;
+      if (b0 + K::NW <= BLOCKS || b < BLOCKS) {
+        const int ib = (b >= 1) + (b >= 3) + (b >= 6);
+        block(ib, b - ib * (ib + 1) / 2);
+      }
+    }
+  };
+
+  if constexpr (PASS == 0) {  // two chunks
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    lds_barrier();
+    scores(lds, sP);
+  } else {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(K::COPIES));
+  }
   lds_barrier();
 
-  const int tr_r = 4 * q4 + (m16 >> 2), tr_g = m16 & 3;
   int slot = 0;
   auto walk = [&](auto near_one) {
   for (int c = sp.c0; c < sp.c1; ++c) {
     const char* bX = lds + slot * K::SB;
     const char* bY = bX + K::AT_Y;
     const char* bZ = bX + K::AT_Z;
-    issue(slot == 0 ? K::NBUF - 1 : slot - 1, c + K::NBUF - 1 < sp.c1);
-    slot = slot + 1 == K::NBUF ? 0 : slot + 1;
+    issue(slot == 0 ? 2 : slot - 1, c + 2 < sp.c1);
+    slot = slot == 2 ? 0 : slot + 1;
+
+    // the next chunk's scores (behind the last chunk there are zeros)
+    if constexpr (PASS == 0) scores(lds + slot * K::SB, sP + (~(c - sp.c0) & 1) * K::PB);
 
     // z columns as fragments over the rows (for two 16-row blocks: rows 4 q4
     // and on of the first, then of the second, as the scores' accumulators lie)
@@ -307,23 +356,6 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
 
     f32x4 O[K::NB];
     if constexpr (PASS == 0) {
-      // this wave's blocks of scores, transposed and masked
-      const int x_row = m16 * (K::GR * 16);
-      for (int b = w; b < K::NB * (K::NB + 1) / 2; b += K::NW) {
-        int ib = 0, jb = b;
-        while (jb > ib) jb -= ++ib;
-        f32x4 P = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < K::NS; ++s) {
-          const int g = (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16;
-          P = Mma<TI>::mma(lds_ld<Frag>(bY + 16 * jb * (K::GR * 16), x_row + g),
-                           lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + g), P);
-        }
-        P *= lds_ld<f32x4>(sD, ((ib - jb) * 64 + lane) * 16);
-        char* at = sP + ((ib * K::NJS + jb / K::TPS) * 64 + lane) * 16;
-        if constexpr (K::B16) lds_st(at, 8 * (jb & 1), cvt4(P));
-        else lds_st(at, 0, P);
-      }
       // the state's part of the outputs, transposed
       Frag Mf[K::NS];
 #pragma unroll
@@ -342,21 +374,18 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
         O[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < K::NS; ++s) {
-          const int g = (((K::SLAB * K::ES / 16) * s + q4) ^ K::swz_y(m16)) * 16;
-          O[ib] = Mma<TI>::mma(Mf[s], lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + g), O[ib]);
+          O[ib] = Mma<TI>::mma(Mf[s], lds_ld<Frag>(bX + 16 * ib * (K::GR * 16), x_row + x_granule(s)), O[ib]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) O[ib][e] *= gam[ib];
       }
-#pragma unroll
-      for (int ib = 0; ib < K::NB; ++ib) settle(O[ib]);  // before the barrier, not behind it
-      lds_barrier();  // the scores are there
+      const char* bP = sP + ((c - sp.c0) & 1) * K::PB;
       // the chunk's own part
 #pragma unroll
       for (int ib = 0; ib < K::NB; ++ib) {
 #pragma unroll
         for (int js = 0; js * K::TPS <= ib; ++js)
-          O[ib] = Mma<TI>::mma(Zf[js], lds_ld<Frag>(sP, ((ib * K::NJS + js) * 64 + lane) * 16), O[ib]);
+          O[ib] = Mma<TI>::mma(Zf[js], lds_ld<Frag>(bP, (K::frag_at(ib, js) * 64 + lane) * 16), O[ib]);
         if constexpr (K::B16)
           __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, cvt4(O[ib])), ro, (int)(o_off + ib * o_blk), 0,
                                                 0);
@@ -425,9 +454,9 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
           for (int v = 0; v < UB; ++v) M[u0 + v] = Mma<TI>::mma(y[v], zt[i], M[u0 + v]);
       }
     }
-    // The next chunk has arrived: behind its copies are, at least, those of
-    // the chunks after it and this chunk's stores.
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm((K::NBUF - 2) * K::COPIES + K::STORES));
+    // With outputs the chunk after the next has to be there, behind whose
+    // copies are this chunk's stores; else the next.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(PASS == 0 ? K::STORES : K::COPIES));
     lds_barrier();
   }
   };
@@ -565,20 +594,14 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
 constexpr int CUS = 256;    // of an MI355X
 constexpr int SEG_MIN = 4;  // chunks a segment has at least
 
-int chunk_rows(int dtype) { return dtype == GDN_BF16 ? 64 : 32; }
-
-// Workgroups of a role of dx x dz that a CU holds: by LDS, and 16 waves.
-int residents(int dx, int dz, int dtype) {
-  const int lds = chunk_rows(dtype) * (3 * dx + dz) * (dtype == GDN_BF16 ? 2 : 4) + 13 * 1024;
-  return std::min(160 * 1024 / lds, 16 * 16 / dz);
-}
+int chunk_rows(int dx, int dz, int dtype) { return (dx == 128 && dz == 128 ? 2 : 1) * (dtype == GDN_BF16 ? 32 : 16); }  // LK::C
 
 // Chunks of a segment, or 0: a sequence is cut where a batch has fewer
 // chains than the device holds workgroups.  What a cut costs is a first
 // launch over y and z, some 0.6 of the second's time a chunk; what it brings
 // is shorter rounds of workgroups.
 int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
-  const long rows = chunk_rows(dtype), chains = (long)B * H * roles, room = CUS;
+  const long rows = chunk_rows(dx, dz, dtype), chains = (long)B * H * roles, room = CUS;
   if (chains <= 0) return 0;
   if (packed) {
     // lengths are not known here: no segment is longer than an even share
@@ -600,9 +623,9 @@ int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, 
   return (int)best;
 }
 
-long segment_slots(int B, int T, bool packed, int segc, int dtype) {
+long segment_slots(int B, int T, bool packed, int segc, int chunk) {
   if (!segc) return B;
-  const long rows = (long)segc * chunk_rows(dtype);
+  const long rows = (long)segc * chunk;
   return packed ? T / rows + B : B * (((long)T + rows - 1) / rows);
 }
 
@@ -626,7 +649,7 @@ int launch_dz(const LinParams& p, int dz, long wgs, hipStream_t s) {
 }
 
 int launch(LinParams p, int dx, int dz, int dtype, hipStream_t s) {
-  const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc, dtype);
+  const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc, chunk_rows(dx, dz, dtype));
   const long wgs = (slots * p.H + 7) / 8 * 8 * p.nrole;
   if (wgs >= 1L << 22) return GDN_ERR_INVALID_ARG;
   p.nslots = (int)slots;
@@ -660,7 +683,7 @@ struct Plan {
 Plan plan(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
   const int segc = segment_chunks(B, T, H, dx, dz, roles, packed, dtype);
   if (!segc) return {0, 0};
-  return {segc, segment_slots(B, T, packed, segc, dtype) * H * roles * dx * dz * 4LL};
+  return {segc, segment_slots(B, T, packed, segc, chunk_rows(dx, dz, dtype)) * H * roles * dx * dz * 4LL};
 }
 
 }  // namespace
