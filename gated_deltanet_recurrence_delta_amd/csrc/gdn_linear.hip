@@ -76,10 +76,12 @@ struct LK {
   static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
   static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
   static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
-  // LDS: three chunks of (x,) y and z, the scores of two chunks, and decays
-  // of scores.
+  // LDS: NBUF chunks of (x,) y and z, the scores of two chunks, and decays of
+  // scores.
   static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, AT_Y = PASS == 0 ? YB : 0, AT_Z = AT_Y + YB, SB = AT_Z + ZB;
-  static constexpr int NBUF = 3;
+  static constexpr int NBUF = PASS == 0 ? 3 : 4;
+  // bf16 terms that the decayed z are taken as where they enter the state
+  static constexpr int TERMS = !B16 ? 1 : (PASS == 0 ? 3 : 2);
   // Fragments of scores, rows 16 ib and on against SLAB columns from SLAB js on.
   __host__ __device__ static constexpr int frag_at(int ib, int js) {
     int n = js;
@@ -89,10 +91,11 @@ struct LK {
   static constexpr int NFR = frag_at(NB, 0), PB = PASS == 0 ? NFR * 1024 : 0, DB = PASS == 0 ? 2048 : 0;
   static constexpr int AT_P = NBUF * SB, AT_D = AT_P + 2 * PB, LDS = AT_D + DB;
   static constexpr int Y_INS = YB / 1024, Z_INS = ZB / 1024;  // copies of 1 KB
+  static constexpr int GROUP = (DX < DZ ? DX : DZ) * ES < 128 ? 2 : 1;  // heads whose rows share a 128-byte line
   // A wave's copies a chunk, at least, and its stores.
   static constexpr int COPIES = (Y_INS >= NW ? (PASS == 0 ? 2 : 1) * Y_INS / NW : 0) + (Z_INS >= NW ? Z_INS / NW : 0);
   static constexpr int STORES = PASS == 0 ? NB : 0;
-  static_assert(COPIES + STORES < 64, "operations in flight are counted in six bits");
+  static_assert(2 * COPIES + STORES < 64, "operations in flight are counted in six bits");
   // In 16-bit storage a transposing read takes four neighbouring values of a
   // row, half a granule.  The halves alternate from granule to granule, so
   // that a read covers all banks: accumulator row m = 4 q + e of tile t of a
@@ -140,8 +143,9 @@ struct Span {
 };
 
 // Rows further back than this many nats of decay are left out of a segment's
-// end state: e^-60 of their own share, far below what 32 bits can add up.
-constexpr double FORGOTTEN = 60.0;
+// end state: e^-40 of their own share, as the halos of the delta rule's
+// segments are bounded.
+constexpr double FORGOTTEN = 40.0;
 
 // 16 bytes a lane from the buffer to LDS, from `at` on.  From assembly: the
 // copy writes LDS only, and as a builtin it would make the compiler wait for
@@ -197,8 +201,8 @@ struct Copier {
 
 // A wave's part.
 template <typename TI, int DX, int DZ, int PASS>
-__device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds,
-                                      const double* sPow, const float* sIn) {
+__device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds, double* sPow,
+                                      float* sIn) {
   using K = LK<TI, DX, DZ, PASS>;
   using Frag = typename K::Frag;
   constexpr int C = K::C;
@@ -223,6 +227,17 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   };
 #pragma unroll
   for (int i = 0; i < K::NBUF - 1; ++i) issue(i, sp.c0 + i < sp.c1);
+
+  // The decay's powers, while the first chunks are on their way.
+  const int tid = threadIdx.x;
+  if (tid <= C) {
+    const double a = pow_of(gh, tid);
+    sPow[tid] = a;
+    sIn[C - tid] = (float)a;
+  } else if (tid < 2 * C) {
+    sIn[tid] = 0.f;
+  }
+  lds_barrier();
 
   // The state: tile u has x rows x_at(u) and on.
   f32x4 M[K::NU];
@@ -326,33 +341,66 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   }
   lds_barrier();
 
-  int slot = 0;
-  auto walk = [&](auto near_one) {
-  for (int c = sp.c0; c < sp.c1; ++c) {
-    const char* bX = lds + slot * K::SB;
-    const char* bY = bX + K::AT_Y;
-    const char* bZ = bX + K::AT_Z;
-    issue(slot == 0 ? 2 : slot - 1, c + 2 < sp.c1);
-    slot = slot == 2 ? 0 : slot + 1;
-
-    // the next chunk's scores (behind the last chunk there are zeros)
-    if constexpr (PASS == 0) scores(lds + slot * K::SB, sP + (~(c - sp.c0) & 1) * K::PB);
-
-    // z columns as fragments over the rows (for two 16-row blocks: rows 4 q4
-    // and on of the first, then of the second, as the scores' accumulators lie)
-    Frag Zf[K::NJS];
+  // A chunk's z columns as fragments over the rows (for two 16-row blocks:
+  // rows 4 q4 and on of the first, then of the second, as the scores'
+  // accumulators lie), and as they enter the state: decayed, in 16-bit
+  // storage as TERMS terms (three are their 24 bits in full).
+  struct ZCols {
+    Frag f[K::NJS], t[K::NJS][K::TERMS];
+  };
+  auto load_z = [&](const char* bZ, ZCols& z) {
 #pragma unroll
     for (int js = 0; js < K::NJS; ++js) {
       if constexpr (K::B16) {
         const char* at = bZ + tr_r * (K::ZGR * 16) + (((2 * w + (tr_g >> 1)) ^ K::swz_z(tr_r)) * 16) + 8 * (tr_g & 1);
         const bf16x4 lo = lds_read_tr(at, 32 * js * (K::ZGR * 16));
         const bf16x4 hi = lds_read_tr(at, (32 * js + 16) * (K::ZGR * 16));
-        Zf[js] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        z.f[js] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) Zf[js][e] = lds_ld<float>(bZ, ((16 * js + 4 * q4 + e) * DZ + z_at) * 4);
+        for (int e = 0; e < 4; ++e) z.f[js][e] = lds_ld<float>(bZ, ((16 * js + 4 * q4 + e) * DZ + z_at) * 4);
       }
     }
+  };
+  auto decay_z = [&](int rows, ZCols& z) {  // rows behind the last have zeros
+    const float* in_pow = sIn + C - (rows - 1 + rev) + 4 * q4;
+#pragma unroll
+    for (int js = 0; js < K::NJS; ++js) {
+      if constexpr (K::B16) {
+        f32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[e] = (float)z.f[js][e] * in_pow[32 * js + e];
+          b[e] = (float)z.f[js][4 + e] * in_pow[32 * js + 16 + e];
+        }
+#pragma unroll
+        for (int i = 0; i < K::TERMS; ++i) {
+          const u32x2 ta = __builtin_bit_cast(u32x2, cvt4(a)), tb = __builtin_bit_cast(u32x2, cvt4(b));
+          z.t[js][i] = __builtin_bit_cast(Frag, u32x4{ta[0], ta[1], tb[0], tb[1]});
+          if (i + 1 < K::TERMS) {
+            a = left_over(a, ta);
+            b = left_over(b, tb);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.t[js][0][e] = z.f[js][e] * in_pow[16 * js + e];
+      }
+    }
+  };
+
+  // One chunk: its outputs and its share of the state; and the next chunk's z
+  // made ready, vector work that runs beside this one's matrix products.
+  int slot = 0;
+  auto chunk = [&](auto near_one, const int c, const ZCols& z, ZCols& zn) {
+    const char* bX = lds + slot * K::SB;
+    const char* bY = bX + K::AT_Y;
+    issue(slot == 0 ? K::NBUF - 1 : slot - 1, c + K::NBUF - 1 < sp.c1);
+    slot = slot == K::NBUF - 1 ? 0 : slot + 1;
+    load_z(lds + slot * K::SB + K::AT_Z, zn);
+
+    // the next chunk's scores (behind the last chunk there are zeros)
+    if constexpr (PASS == 0) scores(lds + slot * K::SB, sP + (~(c - sp.c0) & 1) * K::PB);
 
     f32x4 O[K::NB];
     if constexpr (PASS == 0) {
@@ -385,7 +433,7 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       for (int ib = 0; ib < K::NB; ++ib) {
 #pragma unroll
         for (int js = 0; js * K::TPS <= ib; ++js)
-          O[ib] = Mma<TI>::mma(Zf[js], lds_ld<Frag>(bP, (K::frag_at(ib, js) * 64 + lane) * 16), O[ib]);
+          O[ib] = Mma<TI>::mma(z.f[js], lds_ld<Frag>(bP, (K::frag_at(ib, js) * 64 + lane) * 16), O[ib]);
         if constexpr (K::B16)
           __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, cvt4(O[ib])), ro, (int)(o_off + ib * o_blk), 0,
                                                 0);
@@ -395,37 +443,14 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       o_off += o_step;
     }
 
-    // the state: decayed, and the chunk's y z^T, decayed z in 16-bit storage
-    // as three terms, their 24 bits in full
+    // the state: decayed, and the chunk's y z^T
     const int rows = min(C, len - c * C);
     // a shorter last chunk: its decay is no further from one, or comes once only
     const float last = (float)(decltype(near_one)::value ? sPow[rows] - 1.0 : sPow[rows]);
     apply<decltype(near_one)::value != 0>(rows < C ? last : step.f, M);
-    const float* in_pow = sIn + C - (rows - 1 + rev) + 4 * q4;  // of row 4 q4; rows behind the last have zeros
+    decay_z(max(1, min(C, len - (c + 1) * C)), zn);
 #pragma unroll
     for (int js = 0; js < K::NJS; ++js) {
-      constexpr int TERMS = K::B16 ? 3 : 1;
-      Frag zt[TERMS];
-      if constexpr (K::B16) {
-        f32x4 a, b;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = (float)Zf[js][e] * in_pow[32 * js + e];
-          b[e] = (float)Zf[js][4 + e] * in_pow[32 * js + 16 + e];
-        }
-#pragma unroll
-        for (int i = 0; i < TERMS; ++i) {
-          const u32x2 ta = __builtin_bit_cast(u32x2, cvt4(a)), tb = __builtin_bit_cast(u32x2, cvt4(b));
-          zt[i] = __builtin_bit_cast(Frag, u32x4{ta[0], ta[1], tb[0], tb[1]});
-          if (i + 1 < TERMS) {
-            a = left_over(a, ta);
-            b = left_over(b, tb);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) zt[0][e] = Zf[js][e] * in_pow[16 * js + e];
-      }
       constexpr int UB = K::NU < 4 ? K::NU : 4;  // tiles at a time: independent products one behind another
 #pragma unroll
       for (int u0 = 0; u0 < K::NU; u0 += UB) {
@@ -449,16 +474,26 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
           }
         }
 #pragma unroll
-        for (int i = TERMS - 1; i >= 0; --i)
+        for (int i = K::TERMS - 1; i >= 0; --i)
 #pragma unroll
-          for (int v = 0; v < UB; ++v) M[u0 + v] = Mma<TI>::mma(y[v], zt[i], M[u0 + v]);
+          for (int v = 0; v < UB; ++v) M[u0 + v] = Mma<TI>::mma(y[v], z.t[js][i], M[u0 + v]);
       }
     }
-    // With outputs the chunk after the next has to be there, behind whose
-    // copies are this chunk's stores; else the next.
+    // The chunk after the next has to be there: behind its copies are this
+    // chunk's stores, or the copies of the one after it.
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(PASS == 0 ? K::STORES : K::COPIES));
     lds_barrier();
-  }
+  };
+  auto walk = [&](auto near_one) {
+    ZCols za, zb;
+    load_z(lds + K::AT_Z, za);
+    decay_z(max(1, min(C, len - sp.c0 * C)), za);
+    for (int c = sp.c0; c < sp.c1;) {
+      chunk(near_one, c, za, zb);
+      if (++c >= sp.c1) break;
+      chunk(near_one, c, zb, za);
+      ++c;
+    }
   };
   // One loop for each kind of decay: a choice inside it would cost a copy of the state a chunk.
   if (step.near_one) walk(IC<1>{});
@@ -543,10 +578,11 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
 
   const int tid = threadIdx.x;
   // Consecutive workgroups go to the XCDs in turn: each XCD has every eighth
-  // chain, and the roles of a chain, which read the same rows, are neighbours
-  // on one.
-  const int k = blockIdx.x >> 3;
-  const int chain = k / p.nrole * 8 + (blockIdx.x & 7);
+  // group of chains, and the roles of a chain, which read the same rows, are
+  // neighbours on one.  A group is the heads whose rows share a 128-byte line.
+  constexpr int G = K::GROUP;
+  const int k = blockIdx.x >> 3, kc = k / p.nrole;
+  const int chain = (kc / G * 8 + (blockIdx.x & 7)) * G + kc % G;
   Span sp;
   sp.ri = k % p.nrole;
   if (chain >= p.nslots * p.H) return;
@@ -578,14 +614,6 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
     const double nats = -(double)gh * C;
     if (nats * (sp.c1 - sp.c0) > FORGOTTEN) sp.c0 = max(sp.c0, sp.c1 - 1 - (int)(FORGOTTEN / nats));
   }
-  if (tid <= C) {
-    const double a = pow_of(gh, tid);
-    sPow[tid] = a;
-    sIn[C - tid] = (float)a;
-  } else if (tid < 2 * C) {
-    sIn[tid] = 0.f;
-  }
-  __syncthreads();
   compute<TI, DX, DZ, PASS>(p, sp, gh, __builtin_amdgcn_readfirstlane(tid >> 6), lds, sPow, sIn);
 }
 
@@ -593,6 +621,7 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
 
 constexpr int CUS = 256;    // of an MI355X
 constexpr int SEG_MIN = 4;  // chunks a segment has at least
+constexpr int PACKED_SEG_MIN = 4;
 
 int chunk_rows(int dx, int dz, int dtype) { return (dx == 128 && dz == 128 ? 2 : 1) * (dtype == GDN_BF16 ? 32 : 16); }  // LK::C
 
@@ -602,11 +631,11 @@ int chunk_rows(int dx, int dz, int dtype) { return (dx == 128 && dz == 128 ? 2 :
 // is shorter rounds of workgroups.
 int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
   const long rows = chunk_rows(dx, dz, dtype), chains = (long)B * H * roles, room = CUS;
-  if (chains <= 0) return 0;
+  if (chains <= 0 || T == 0) return 0;
   if (packed) {
     // lengths are not known here: no segment is longer than an even share
     const long all = ((long)T + rows - 1) / rows;
-    const long share = std::max<long>(SEG_MIN, (all * H * roles + room - 1) / room);
+    const long share = std::max<long>(PACKED_SEG_MIN, (all * H * roles + room - 1) / room);
     return share < all ? (int)share : 0;
   }
   const long nch = ((long)T + rows - 1) / rows;
@@ -650,7 +679,7 @@ int launch_dz(const LinParams& p, int dz, long wgs, hipStream_t s) {
 
 int launch(LinParams p, int dx, int dz, int dtype, hipStream_t s) {
   const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc, chunk_rows(dx, dz, dtype));
-  const long wgs = (slots * p.H + 7) / 8 * 8 * p.nrole;
+  const long wgs = (slots * p.H + 15) / 16 * 16 * p.nrole;  // whole groups on each of the eight XCDs
   if (wgs >= 1L << 22) return GDN_ERR_INVALID_ARG;
   p.nslots = (int)slots;
   p.nseg = p.segc && !p.cu ? (int)(slots / p.B) : 1;

@@ -7,6 +7,8 @@ as in the package's other entry points.
 """
 from __future__ import annotations
 
+import functools
+
 from . import GDN_BF16, GDN_F32, GdnError, load, strerror
 
 __all__ = ["gdn_linear_fwd", "gdn_linear_fwd_recurrent", "gdn_linear_bwd", "gdn_linear_workspace_size",
@@ -39,6 +41,11 @@ def gdn_linear_workspace_size(B, T, H, dk, dv, packed, dtype, backward=False) ->
                                             int(backward))
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(B, T, H, dk, dv, packed, dtype, backward):
+    return gdn_linear_workspace_size(B, T, H, dk, dv, packed, dtype, backward)
+
+
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -47,30 +54,31 @@ def _sizes(q, k, v, cu_seqlens):
     """(dtype code, B, T, H, dk, dv) of a call's token tensors, checked against one another."""
     import torch
 
-    if q.dtype == torch.bfloat16:
+    qt, qs, vs = q.dtype, q.shape, v.shape
+    if qt == torch.bfloat16:
         dtype = GDN_BF16
-    elif q.dtype == torch.float32:
+    elif qt == torch.float32:
         dtype = GDN_F32
     else:
-        raise TypeError(f"q/k/v dtype must be float32 or bfloat16, got {q.dtype}")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError(f"q/k/v must share one dtype, got {q.dtype}, {k.dtype}, {v.dtype}")
+        raise TypeError(f"q/k/v dtype must be float32 or bfloat16, got {qt}")
+    if k.dtype != qt or v.dtype != qt:
+        raise TypeError(f"q/k/v must share one dtype, got {qt}, {k.dtype}, {v.dtype}")
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int32:
             raise TypeError("cu_seqlens must be int32")
-        if q.dim() != 3:
+        if len(qs) != 3:
             raise ValueError("packed q must be (T, H, dk)")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be one-dimensional, with at least one entry")
-        T, H, dk = q.shape
+        T, H, dk = qs
         B = cu_seqlens.numel() - 1
     else:
-        if q.dim() != 4:
+        if len(qs) != 4:
             raise ValueError("q must be (B, T, H, dk)")
-        B, T, H, dk = q.shape
-    if k.shape != q.shape or v.dim() != q.dim() or v.shape[:-1] != q.shape[:-1]:
+        B, T, H, dk = qs
+    if k.shape != qs or len(vs) != len(qs) or vs[:-1] != qs[:-1]:
         raise ValueError("q, k, v shapes disagree")
-    return dtype, B, T, H, dk, v.shape[-1]
+    return dtype, B, T, H, dk, vs[-1]
 
 
 def _placed(dev, tensors):
@@ -78,22 +86,42 @@ def _placed(dev, tensors):
     if dev.type != "cuda":
         raise ValueError("all tensors must be on the same GPU device")
     for t in tensors:
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError("all tensors must be on the same GPU device")
-        if not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous")
+        if t is not None:
+            if t.device != dev:
+                raise ValueError("all tensors must be on the same GPU device")
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
 
 
 def _like(name, t, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _ok(rc, call):
+def _raw_stream(dev, stream):
+    """The handle of ``stream``, or of ``dev``'s current stream."""
+    import torch
+
+    if stream is not None:
+        return stream.cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev.index)  # without the Stream object around it
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(name, dev, *args):
+    """The C entry point ``name`` with ``dev`` as the current device; raises on its status."""
+    import torch
+
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
     if rc != 0:
-        raise GdnError(rc, strerror(rc), call)
+        raise GdnError(rc, strerror(rc), name)
 
 
 def _decays(g, H):
@@ -105,7 +133,7 @@ def _decays(g, H):
 
 
 def _scratch(need, workspace, dev, stream):
-    """The call's workspace: the caller's, or one from ``stream``'s own memory."""
+    """The call's workspace: the caller's, or one from the memory of the stream it runs on."""
     import torch
 
     if need < 0:
@@ -113,8 +141,11 @@ def _scratch(need, workspace, dev, stream):
     if workspace is None:
         if need == 0:
             return None, 0
-        with torch.cuda.stream(stream):
+        if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on q's device and hold {need} bytes")
@@ -130,8 +161,6 @@ def _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream):
     _placed(dev, (q, k, v, g, h0, cu_seqlens, out, hT))
     if h0 is not None:
         _like("h0", h0, (B, H, dk, dv), torch.float32)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     if out is None:
         out = torch.empty_like(v)
     else:
@@ -141,8 +170,8 @@ def _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream):
     else:
         _like("hT", hT, (B, H, dk, dv), torch.float32)
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(cu_seqlens), out.data_ptr(),
-            hT.data_ptr(), B, T, H, dk, dv, stream.cuda_stream, dtype)
-    return args, out, hT, stream
+            hT.data_ptr(), B, T, H, dk, dv, _raw_stream(dev, stream), dtype)
+    return args, out, hT
 
 
 def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None, stream=None, workspace=None):
@@ -157,24 +186,17 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None, stream=N
     ``workspace``: a uint8 device tensor of at least
     ``gdn_linear_workspace_size`` bytes, allocated here when None.
     """
-    import torch
-
-    args, out, hT, stream = _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream)
-    B, T, H, dk, dv = args[8:13]
-    need = gdn_linear_workspace_size(B, T, H, dk, dv, cu_seqlens is not None, args[14])
+    args, out, hT = _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream)
+    need = _workspace_bytes(*args[8:13], cu_seqlens is not None, args[14], False)
     ws, size = _scratch(need, workspace, q.device, stream)
-    with torch.cuda.device(q.device):
-        _ok(gdn_linear_fwd(*args, _ptr(ws), size), "gdn_linear_fwd")
+    _call("gdn_linear_fwd", q.device, *args, _ptr(ws), size)
     return out, hT
 
 
 def linear_fwd_recurrent(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None, stream=None):
     """Token-by-token form of ``linear_fwd`` (decoding and short sequences)."""
-    import torch
-
-    args, out, hT, stream = _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream)
-    with torch.cuda.device(q.device):
-        _ok(gdn_linear_fwd_recurrent(*args), "gdn_linear_fwd_recurrent")
+    args, out, hT = _forward_args(q, k, v, g, h0, cu_seqlens, out, hT, stream)
+    _call("gdn_linear_fwd_recurrent", q.device, *args)
     return out, hT
 
 
@@ -201,18 +223,14 @@ def _backward(q, k, v, g, dout, h0, cu_seqlens, dhT, want_dh0, workspace, stream
         if t is not None:
             _like(name, t, (B, H, dk, dv), torch.float32)
     _placed(dev, (q, k, v, g, h0, cu_seqlens, dout, dhT))
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    need = gdn_linear_workspace_size(B, T, H, dk, dv, cu_seqlens is not None, dtype, True)
+    need = _workspace_bytes(B, T, H, dk, dv, cu_seqlens is not None, dtype, True)
     ws, size = _scratch(need, workspace, dev, stream)
     new = torch.zeros_like if clear else torch.empty_like
     grads = {"dq": new(q), "dk": new(k), "dv": new(v),
              "dh0": torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None}
-    with torch.cuda.device(dev):
-        rc = gdn_linear_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens), _ptr(dout), _ptr(dhT),
-                            _ptr(grads["dq"]), _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["dh0"]), B, T, H,
-                            dk, dv, stream.cuda_stream, dtype, _ptr(ws), size)
-    _ok(rc, "gdn_linear_bwd")
+    _call("gdn_linear_bwd", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens), _ptr(dout), _ptr(dhT),
+          _ptr(grads["dq"]), _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["dh0"]), B, T, H, dk, dv,
+          _raw_stream(dev, stream), dtype, _ptr(ws), size)
     return grads
 
 

@@ -2,10 +2,11 @@
 token-by-token forms on states in slots, and the moving of slots."""
 from __future__ import annotations
 
-import ctypes
+import math
+from array import array
 
-from . import load
-from .linear import _decays, _like, _ok, _placed, _ptr, _sizes
+from . import GdnError, load
+from .linear import _call, _decays, _like, _placed, _ptr, _raw_stream, _sizes
 
 __all__ = ["gdn_fwd_recurrent_pool", "gdn_linear_fwd_recurrent_pool", "gdn_state_move", "fwd_recurrent_pool",
            "linear_fwd_recurrent_pool", "state_move", "StatePool"]
@@ -26,7 +27,7 @@ def gdn_linear_fwd_recurrent_pool(q, k, v, g, pool, slots, cu_seqlens, out, nslo
 
 
 def gdn_state_move(pool, outer, slots, slot_bytes, src, dst, n, stream) -> int:
-    """Raw C call of the slot moves; ``src`` and ``dst`` are host int32 arrays (ctypes).  Returns the status."""
+    """Raw C call of the slot moves; ``src`` and ``dst`` are host int32 arrays (their addresses, or ctypes arrays).  Returns the status."""
     return load().gdn_state_move(pool, int(outer), int(slots), int(slot_bytes), src, dst, int(n), stream)
 
 
@@ -45,9 +46,7 @@ def _pooled(q, k, v, pool, slots, cu_seqlens, out, stream, more):
         out = torch.empty_like(v)
     else:
         _like("out", out, v.shape, v.dtype)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    return (pool.shape[0], B, T, H, dk, dv, stream.cuda_stream, dtype), out
+    return (pool.shape[0], B, T, H, dk, dv, _raw_stream(dev, stream), dtype), out
 
 
 def fwd_recurrent_pool(q, k, v, g, beta, pool, slots, cu_seqlens=None, out=None, stream=None):
@@ -63,35 +62,42 @@ def fwd_recurrent_pool(q, k, v, g, beta, pool, slots, cu_seqlens=None, out=None,
     for name, t in (("g", g), ("beta", beta)):
         _like(name, t, q.shape[:-1], torch.float32)
     sizes, out = _pooled(q, k, v, pool, slots, cu_seqlens, out, stream, (g, beta))
-    with torch.cuda.device(q.device):
-        rc = gdn_fwd_recurrent_pool(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                    pool.data_ptr(), slots.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), *sizes)
-    _ok(rc, "gdn_fwd_recurrent_pool")
+    _call("gdn_fwd_recurrent_pool", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+          pool.data_ptr(), slots.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), *sizes)
     return out
 
 
 def linear_fwd_recurrent_pool(q, k, v, g, pool, slots, cu_seqlens=None, out=None, stream=None):
     """``linear_fwd_recurrent`` on states in a pool; pool and slots as for
     ``fwd_recurrent_pool``, g: (H,) float32.  Returns out."""
-    import torch
-
     _decays(g, q.shape[-2])
     sizes, out = _pooled(q, k, v, pool, slots, cu_seqlens, out, stream, (g,))
-    with torch.cuda.device(q.device):
-        rc = gdn_linear_fwd_recurrent_pool(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), pool.data_ptr(),
-                                           slots.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), *sizes)
-    _ok(rc, "gdn_linear_fwd_recurrent_pool")
+    _call("gdn_linear_fwd_recurrent_pool", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+          pool.data_ptr(), slots.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), *sizes)
     return out
 
 
 def _host_ints(name, x):
-    """A list of ints from a list, a range, a NumPy array or a CPU tensor."""
-    if getattr(x, "is_cuda", False):
-        raise TypeError(f"{name} must be on the host: the slots' owner knows them there")
-    x = x.tolist() if hasattr(x, "tolist") else list(x)
-    if any(type(i) is not int for i in x):
-        raise TypeError(f"{name} must be a sequence of ints")
-    return x
+    """An int32 array from a list, a range, a NumPy array or a CPU tensor."""
+    if type(x) is not list:
+        if getattr(x, "is_cuda", False):
+            raise TypeError(f"{name} must be on the host: the slots' owner knows them there")
+        x = x.tolist() if hasattr(x, "tolist") else list(x)
+    try:
+        return array("i", x)
+    except OverflowError:
+        raise ValueError(f"{name} holds a number that is no slot") from None
+    except TypeError:
+        raise TypeError(f"{name} must be a sequence of ints") from None
+
+
+def _check_moves(src, dst, slots):
+    if len(src) != len(dst):
+        raise ValueError(f"src and dst must have one length, got {len(src)} and {len(dst)}")
+    if src and (min(src) < -1 or max(src) >= slots or min(dst) < 0 or max(dst) >= slots):
+        raise ValueError(f"slots must lie in [0, {slots}) (src: or be -1)")
+    if len(set(dst)) != len(dst):
+        raise ValueError("a target may be written once only")
 
 
 def state_move(pool, src, dst, dim=0, stream=None):
@@ -104,34 +110,24 @@ def state_move(pool, src, dst, dim=0, stream=None):
     the host, no target twice.  In place, on the current stream (or
     ``stream``); returns pool.
     """
-    import torch
-
     src, dst = _host_ints("src", src), _host_ints("dst", dst)
-    if len(src) != len(dst):
-        raise ValueError(f"src and dst must have one length, got {len(src)} and {len(dst)}")
-    if not -pool.dim() <= dim < pool.dim():
+    shape = pool.shape
+    if not -len(shape) <= dim < len(shape):
         raise ValueError(f"pool has no dimension {dim}")
-    dim %= pool.dim()
-    slots = pool.shape[dim]
-    if src and (min(src) < -1 or max(src) >= slots or min(dst) < 0 or max(dst) >= slots):
-        raise ValueError(f"slots must lie in [0, {slots}) (src: or be -1)")
-    if len(set(dst)) != len(dst):
-        raise ValueError("a target may be written once only")
-    _placed(pool.device, (pool,))
-    outer, size = 1, pool.element_size()
-    for n in pool.shape[:dim]:
-        outer *= n
-    for n in pool.shape[dim + 1:]:
-        size *= n
-    if pool.numel() == 0 or not src:
+    dim %= len(shape)
+    slots, n, dev = shape[dim], len(src), pool.device
+    if n != len(dst) or n > slots or pool.numel() == 0:
+        _check_moves(src, dst, slots)
+    _placed(dev, (pool,))
+    if n == 0 or pool.numel() == 0:
         return pool
-    if stream is None:
-        stream = torch.cuda.current_stream(pool.device)
-    array = ctypes.c_int32 * len(src)
-    with torch.cuda.device(pool.device):
-        rc = gdn_state_move(pool.data_ptr(), outer, slots, size, array(*src), array(*dst), len(src),
-                            stream.cuda_stream)
-    _ok(rc, "gdn_state_move")
+    try:
+        _call("gdn_state_move", dev, pool.data_ptr(), math.prod(shape[:dim]), slots,
+              math.prod(shape[dim + 1:]) * pool.element_size(), src.buffer_info()[0], dst.buffer_info()[0], n,
+              _raw_stream(dev, stream))
+    except GdnError:
+        _check_moves(src, dst, slots)  # says which of the arguments it was
+        raise
     return pool
 
 
@@ -163,7 +159,7 @@ class StatePool:
         return len(self._free)
 
     def _check(self, slots):
-        slots = _host_ints("slots", slots)
+        slots = _host_ints("slots", slots).tolist()
         for s in slots:
             if s not in self._live:
                 raise ValueError(f"slot {s} is not in use")
@@ -197,7 +193,7 @@ class StatePool:
 
     def copy(self, src, dst):
         """State of src[i] into dst[i], all at once; slots in use."""
-        src, dst = _host_ints("src", src), self._check(dst)
+        src, dst = _host_ints("src", src).tolist(), self._check(dst)
         self._check(set(src))
         if len(src) != len(dst):
             raise ValueError("src and dst must have one length")

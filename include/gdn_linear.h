@@ -64,13 +64,23 @@ extern "C" {
  * batch is cut into segments goes by B, T, H, dv alone, so the same sequence
  * in another batch may differ by rounding.
  *
+ * Segments.  A long sequence of a batch with fewer chains than the device has
+ * compute units is cut into segments that run side by side.  A first launch
+ * forms the state that each segment leaves, from which the next ones start;
+ * rows whose decay to the segment's end is below e^-40 are left out of it (as
+ * gdn_fwd's halos are bounded), non-finite ones among them.  With hT == h0
+ * nothing is cut.
+ *
  * Arithmetic: GDN_BF16: every product on the bf16 matrix cores with fp32
  * accumulation; the masked scores and the state are rounded to bf16 as
- * operands of the outputs only, and the decayed values that go into the
- * state are taken as two bf16 terms (16 significant bits), so hT keeps
- * about 2^-17 of its scale.  GDN_F32: fp32 throughout.  The state is carried
- * in fp32 in both.  Non-finite inputs propagate within their own head and
- * sequence, to rows of the same 64-row chunk before them too.
+ * operands of the outputs only, and the decayed values that enter the state
+ * are taken as three bf16 terms, all of their 24 bits (as two terms, 16 bits,
+ * in a segment that others follow).  GDN_F32: fp32 throughout.  The state is
+ * carried in fp32 in both, and a constant decay's rounding does not add up
+ * over a long sequence.  Non-finite inputs propagate within their own head
+ * and sequence, to the rows of the same chunk (64 rows at most) before them
+ * too.  A positive g is computed as it stands, as long as the powers over 64
+ * rows are finite.
  */
 int gdn_linear_fwd(const void* q, const void* k, const void* v, const float* g,
                    const float* h0, const int32_t* cu_seqlens, void* out,

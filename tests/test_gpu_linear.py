@@ -361,3 +361,41 @@ def test_refused_on_the_gpu():
         gdn.linear_fwd(c["q"], c["k"], c["v"], c["g"], out=c["v"])
     with pytest.raises(ValueError):
         gdn.linear_fwd(c["q"], c["k"], c["v"], c["g"], out=torch.empty(1, 40, 2, 32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_tokens(dtype):
+    """Sequences of no tokens hand their states on, in both directions."""
+    c = make(13, dtype, 0, 2, 64, 64, 3)
+    got = run_all(c)
+    assert torch.equal(got["hT"], c["h0"]) and torch.equal(got["dh0"], c["dhT"]) and got["out"].numel() == 0
+    out, hT = gdn.linear_fwd_recurrent(c["q"], c["k"], c["v"], c["g"])
+    assert not bool(hT.any()) and out.shape == c["v"].shape
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [511, 700])
+def test_many_packed_sequences(dtype, B):
+    """More sequences than are put in order of length, and just fewer; some long enough to be cut."""
+    r = np.random.default_rng(B)
+    lens = r.integers(0, 5, B)
+    lens[[3, B // 2, B - 1]] = [400, 333, 129]
+    bounds = [0, *np.cumsum(lens).tolist()]
+    c = make(B, dtype, bounds[-1], 1, 32, 32, B, packed=True, slow=True)
+    check(run_all(c, torch.tensor(bounds, dtype=torch.int32, device="cuda")), c, dtype, bounds)
+
+
+@pytest.mark.parametrize("dk,dv", [(32, 32), (128, 128)])
+@pytest.mark.parametrize("H", [1, 7, 19])
+def test_odd_heads(dk, dv, H):
+    c = make(H, "bf16", 70, H, dk, dv, 3)
+    check(run_all(c), c, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_far_rows_are_left_out_of_cut_sequences(dtype):
+    """A fast decay in a cut sequence: what is left out is below e^-40 of its own size."""
+    c = make(14, dtype, 3000, 2, 64, 64, 1)
+    c["g"].copy_(torch.tensor([-0.5, -8.0]))
+    assert gdn.gdn_linear_workspace_size(1, 3000, 2, 64, 64, 0, gdn.GDN_BF16) > 0
+    check(run_all(c), c, dtype)

@@ -116,6 +116,10 @@ def test_workspace():
     assert need > 0 and need % (2 * 128 * 128 * 4) == 0
     assert size(3, 32768, 2, 128, 128, 1, 1) > 0
     assert size(1, 32768, 2, 128, 64, 0, 1, 1) > 0
+    for packed in (0, 1):
+        for backward in (0, 1):  # no rows, no sequences
+            assert size(3, 0, 2, 128, 64, packed, 1, backward) == 0
+            assert size(0, 100, 2, 64, 64, packed, 0, backward) == 0
     assert size(1, 32768, 0, 128, 128, 0, 1) == INVALID
     assert size(1, 32768, 2, 48, 128, 0, 1) == UNSUPPORTED
     a = dict(B=1, T=32768, H=2, dk=128, dv=128)
