@@ -20,17 +20,28 @@
 //   O = P Z + diag(a^(i+1)) X S,   S <- a^C S + (diag(a^(C-1-j)) Y)^T Z.
 //
 // A workgroup walks the chunks of one chain (or of a segment of it) with the
-// whole state in registers: each computing wave owns 16 state columns, all
-// dx rows of them, so the state's accumulators are the outputs' operand as
-// they stand and nothing of the state goes through LDS.  The scores are
-// formed transposed, Y X^T, so that their accumulators are an operand too;
-// their 16 x 16 blocks are shared out among the waves and handed over
-// through LDS.  One more wave copies the chunks of x, y and z to LDS, two
-// chunks ahead: every row is read from memory once, and the matrix cores
-// have four times the time that the products need at dx = dz = 128.
-// (Workgroups of 32 state columns each, four to a chain, need no segments at
-// 64 chains, but read x and y four times over: from L2 that goes at 11 TB/s,
-// and B=4 H=16 T=4096 took 98 us that way.)
+// whole state in registers: each wave owns 16 state columns, all dx rows of
+// them, so the state's accumulators are the outputs' operand as they stand
+// and nothing of the state goes through LDS.  The scores are formed
+// transposed, Y X^T, so that their accumulators are an operand too; their
+// 16 x 16 blocks are shared out among the waves and handed over through LDS,
+// one chunk ahead of their use.  The waves copy the rows to LDS themselves,
+// two chunks ahead, and one barrier a chunk hands over rows and scores.
+//
+// Bound by memory: every row is read once by one workgroup, or twice where
+// its chain is cut (two launches, see segment_chunks).  B=4 H=16 T=4096,
+// dx = dz = 128 bf16: 37 us for the segments' states, 61 us for the outputs,
+// 64 KB for each 64 rows of a workgroup in 3.2 us, 5.1 TB/s over the device (a
+// copy of the same size reaches 4.7); 11 us of each launch are its start, the
+// first chunks' way and the last stores.  512 chains uncut (2.1 GB): 479 us,
+// 4.5 TB/s.
+//
+// What was tried in its place, for the same call: workgroups of 32 state
+// columns, four to a chain, need no segments, but read x and y four times
+// over, which L2 gives at 11 TB/s and no more: 98 us in one launch.  Two
+// workgroups on a CU with half the rows in flight each: 71 us for the
+// outputs.  A wave of its own for the copies, scores behind a barrier of
+// their own: 66 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -69,10 +80,12 @@ struct LK {
   using Frag = typename Mma<TI>::frag;
   static constexpr bool B16 = sizeof(TI) == 2;
   static constexpr int ES = sizeof(TI), SLAB = Mma<TI>::SLAB, E = Mma<TI>::E;
-  // Rows of a chunk, 16-row blocks: the longest that leaves three chunks in
-  // LDS for the largest states, half of that for the others, whose fewer
-  // waves need more workgroups on a CU.
-  static constexpr int C = (DX == 128 && DZ == 128 ? 2 : 1) * (B16 ? 32 : 16), NB = C / 16;
+  // Rows of a chunk, 16-row blocks.  bf16: 32 (64 rows at dx = dz = 128 take
+  // 272 us where these take 260, 64,711 packed rows of 16 heads).  fp32: 16,
+  // which leaves room for two workgroups on a CU (dx = 128, dz = 32, 512
+  // chains of 4,096 rows: 594 us, with 32 rows 1,089), but 32 at 128 x 128,
+  // where there is room for one either way (700 us against 766).
+  static constexpr int C = B16 || (DX == 128 && DZ == 128) ? 32 : 16, NB = C / 16;
   static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
   static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
   static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
@@ -201,8 +214,8 @@ struct Copier {
 
 // A wave's part.
 template <typename TI, int DX, int DZ, int PASS>
-__device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds, double* sPow,
-                                      float* sIn) {
+__device__ static inline void compute(const LinParams& p, const Span& sp, const float gh, const int w, char* lds,
+                                      double* sPow, float* sIn) {
   using K = LK<TI, DX, DZ, PASS>;
   using Frag = typename K::Frag;
   constexpr int C = K::C;
@@ -219,7 +232,8 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   const long x0 = sp.th0 * DX * K::ES;
   Copier<K::Y_INS, K::NW, K::GR> cx(role.x + x0, x_stride, len, rev, row0, C, w, lds, place_y);
   Copier<K::Y_INS, K::NW, K::GR> cy(role.y + x0, x_stride, len, rev, row0, C, w, lds + K::AT_Y, place_y);
-  Copier<K::Z_INS, K::NW, K::ZGR> cz(role.z + sp.th0 * DZ * K::ES, z_stride, len, rev, row0, C, w, lds + K::AT_Z, place_z);
+  Copier<K::Z_INS, K::NW, K::ZGR> cz(role.z + sp.th0 * DZ * K::ES, z_stride, len, rev, row0, C, w, lds + K::AT_Z,
+                                     place_z);
   auto issue = [&](int slot, bool in) {
     if constexpr (PASS == 0) cx.issue(slot * K::SB, in);
     cy.issue(slot * K::SB, in);
@@ -294,7 +308,7 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = 16 * d + m16 - 4 * q4 - e;
-        v[e] = n >= 0 ? (float)pow_of(gh, n) : 0.f;
+        v[e] = n >= 0 ? (float)sPow[min(n, C)] : 0.f;  // past C: beside the diagonal of a chunk of one block, unused
       }
       lds_st(sD, (d * 64 + lane) * 16, v);
     }
@@ -312,11 +326,10 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
 #pragma unroll
       for (int s = 0; s < K::NS; ++s)
         P = Mma<TI>::mma(lds_ld<Frag>(bY, x_row + x_granule(s)), lds_ld<Frag>(bX, x_row + x_granule(s)), P);
-      const int d = ib - jb;
-      const f32x4 decay = lds_ld<f32x4>(sD, ((d > 0) * 64 + lane) * 16);
-      const float more = sIn[C - (d > 1 ? 16 * (d - 1) : 0)];
+      static_assert(K::NB <= 2, "two tables of decays");
+      const f32x4 decay = lds_ld<f32x4>(sD, ((ib - jb) * 64 + lane) * 16);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) P[e] = P[e] * decay[e] * more;
+      for (int e = 0; e < 4; ++e) P[e] *= decay[e];
       char* at = to + (K::frag_at(ib, jb / K::TPS) * 64 + lane) * 16;
       if constexpr (K::B16) lds_st(at, 8 * (jb & 1), cvt4(P));
       else lds_st(at, 0, P);
@@ -326,7 +339,7 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
     for (int b0 = 0; b0 < BLOCKS; b0 += K::NW) {
       const int b = b0 + w;
       if (b0 + K::NW <= BLOCKS || b < BLOCKS) {
-        const int ib = (b >= 1) + (b >= 3) + (b >= 6);
+        const int ib = b >= 1;
         block(ib, b - ib * (ib + 1) / 2);
       }
     }
@@ -623,7 +636,7 @@ constexpr int CUS = 256;    // of an MI355X
 constexpr int SEG_MIN = 4;  // chunks a segment has at least
 constexpr int PACKED_SEG_MIN = 4;
 
-int chunk_rows(int dx, int dz, int dtype) { return (dx == 128 && dz == 128 ? 2 : 1) * (dtype == GDN_BF16 ? 32 : 16); }  // LK::C
+int chunk_rows(int dx, int dz, int dtype) { return dtype == GDN_BF16 || (dx == 128 && dz == 128) ? 32 : 16; }  // LK::C
 
 // Chunks of a segment, or 0: a sequence is cut where a batch has fewer
 // chains than the device holds workgroups.  What a cut costs is a first

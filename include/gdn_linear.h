@@ -78,8 +78,8 @@ extern "C" {
  * in a segment that others follow).  GDN_F32: fp32 throughout.  The state is
  * carried in fp32 in both, and a constant decay's rounding does not add up
  * over a long sequence.  Non-finite inputs propagate within their own head
- * and sequence, to the rows of the same chunk (64 rows at most) before them
- * too.  A positive g is computed as it stands, as long as the powers over 64
+ * and sequence, to the rows of the same chunk (32 rows at most) before them
+ * too.  A positive g is computed as it stands, as long as the powers over 32
  * rows are finite.
  */
 int gdn_linear_fwd(const void* q, const void* k, const void* v, const float* g,

@@ -4,9 +4,9 @@ Tolerances come from the arithmetic.  With A the same sums over absolute
 values (the oracle on |q|, |k|, |v|, |h0|), every rounding of relative size r
 to a term of a sum moves the sum by at most r A:
 
-- fp32 sums of n terms: n 2^-24 A, n the row width, the chunk's 64 rows and
-  four steps (decay, its low term, joining, rounding) a chunk; decay powers
-  are within 2^-24;
+- fp32 sums of n terms: n 2^-24 A, n the row width, a chunk's rows (64 at
+  most) and four roundings for each 64 rows on the way; decay powers are
+  within 2^-24;
 - bf16: the masked scores or the state, and (for the outputs) the products'
   other operand being exact, one rounding of 2^-8 A, and the output's own
   2^-8 |out|; values that enter the state are kept as two bf16 terms,
@@ -101,7 +101,7 @@ DIMS = [(32, 32), (64, 64), (128, 128), (128, 32), (32, 64), (64, 128)]
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", DIMS)
-@pytest.mark.parametrize("T", [1, 16, 63, 64, 65, 130, 321])
+@pytest.mark.parametrize("T", [1, 16, 31, 32, 33, 63, 64, 65, 130, 321])
 def test_dense(dtype, dk, dv, T):
     c = make(T * 7 + dk + dv, dtype, T, 3, dk, dv, 2)
     check(run_all(c), c, dtype)

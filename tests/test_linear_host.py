@@ -111,7 +111,7 @@ def test_overlapping_outputs():
 def test_workspace():
     size = gdn.gdn_linear_workspace_size
     assert size(64, 4096, 16, 128, 128, 0, 1) == 0  # enough chains: nothing is cut
-    assert size(1, 512, 1, 128, 128, 0, 1) == 0  # too short
+    assert size(1, 200, 1, 128, 128, 0, 1) == 0  # too short
     need = size(1, 32768, 2, 128, 128, 0, 1)
     assert need > 0 and need % (2 * 128 * 128 * 4) == 0
     assert size(3, 32768, 2, 128, 128, 1, 1) > 0
