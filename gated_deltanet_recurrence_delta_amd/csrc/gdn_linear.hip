@@ -71,7 +71,7 @@ struct LinParams {
   f32x4* ws;          // end states of the segments
   int B, T, H, nrole;
   int segc;           // chunks of a segment; 0: nothing is cut
-  int nslots;         // (sequence, segment) slots
+  int nslots;         // places of (sequence, segment)
   int nseg;           // of them a dense sequence's
 };
 
@@ -526,44 +526,62 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   }
 }
 
-constexpr int SORTED = 512;  // sequences of a packed batch that are put in order of length
+// The begin and length of a packed batch's sequence, within the rows there are.
+struct Rows {
+  int begin, len;
+};
+__device__ static inline Rows rows_of(const LinParams& p, int i) {
+  const int b = min(max(p.cu[i], 0), p.T);
+  return {b, min(max(p.cu[i + 1], b), p.T) - b};
+}
 
-// The (sequence, segment) of a packed batch that comes at place `at`: whole
-// segments first, then the sequences' last ones from long to short, so that
-// the workgroups that start late are short.  False: there is none.
-template <int NT>
+constexpr int SORTED = 64;  // sequences of a packed batch that are put in order of length
+
+// The (sequence, segment) that comes at place `at` of a packed batch cut into
+// segments of `rows` rows; false: there is none.
+//
+// PASS 1 goes by the slots of the segments that others follow: a sequence's
+// are floor(begin / rows) and on, as many as whole segments fit in it at most,
+// so that the sequences' slots are apart and below floor(T / rows).
+//
+// PASS 0 takes whole segments first and then the sequences' last ones from
+// long to short, so that the workgroups that start late are short ones
+// (64,711 rows in 32 sequences of 16 heads, dx = dz = 128: 252 us, in the
+// order of the batch 338).  With more sequences the order matters less and
+// costs more (50,000 rows in 100: 232 against 225), and sequence i has the
+// places floor(begin / rows) + i and on.
+template <int PASS, int NT>
 __device__ static inline bool packed_span(const LinParams& p, int rows, int at, int* lds, int& n, int& seg) {
   const int tid = threadIdx.x;
-  int* found = lds + SORTED;
+  int *found = lds, *whole = lds + 2, *rest = whole + SORTED;
   if (tid == 0) found[0] = -1;
-  auto len_of = [&](int i) {
-    const int b = min(max(p.cu[i], 0), p.T);
-    return min(max(p.cu[i + 1], b), p.T) - b;
-  };
-  if (p.B <= SORTED) {
-    for (int i = tid; i < p.B; i += NT) lds[i] = len_of(i);
+  if (PASS == 0 && p.B <= SORTED) {
+    for (int i = tid; i < p.B; i += NT) {
+      const int len = rows_of(p, i).len;
+      whole[i] = len / rows;
+      rest[i] = len % rows > 0 || len == 0 ? len % rows : -1;  // -1: whole segments alone
+    }
     __syncthreads();
     for (int i = tid; i < p.B; i += NT) {
-      // the last segment is a short one, unless the length divides evenly
-      const int len = lds[i], whole = len / rows, rest = len - whole * rows;
-      const bool has_rest = rest > 0 || len == 0;
+      const int wi = whole[i], ri = rest[i];
       int before = 0, all = 0, longer = 0;
       for (int j = 0; j < p.B; ++j) {
-        const int l = lds[j], wj = l / rows, rj = l - wj * rows;
+        const int wj = whole[j], rj = rest[j];
         all += wj;
         before += j < i ? wj : 0;
-        longer += (rj > 0 || l == 0) && (rj > rest || (rj == rest && j < i));
+        longer += rj > ri || (rj == ri && j < i);
       }
-      const int s = at < all ? at - before : (has_rest && at - all == longer ? whole : -1);
-      if (s >= 0 && (at >= all || s < whole)) {
+      if (at < all ? at >= before && at < before + wi : ri >= 0 && at - all == longer) {
         found[0] = i;
-        found[1] = s;
+        found[1] = at < all ? at - before : wi;
       }
     }
-  } else {  // too many to be sorted: sequence i has places floor(begin / rows) + i and on
+  } else {
     __syncthreads();
     for (int i = tid; i < p.B; i += NT) {
-      const int first = min(max(p.cu[i], 0), p.T) / rows + i, count = max(1, (len_of(i) + rows - 1) / rows);
+      const Rows r = rows_of(p, i);
+      const int segs = (r.len + rows - 1) / rows;
+      const int first = r.begin / rows + (PASS == 0 ? i : 0), count = PASS == 0 ? max(1, segs) : segs - 1;
       if (at >= first && at < first + count) {
         found[0] = i;
         found[1] = at - first;
@@ -587,7 +605,7 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   __shared__ double sPow[C + 1];
   __shared__ float sIn[2 * C];  // the decay's powers from C down to 0, then zeros
   static_assert(K::NT >= 2 * C, "a thread for each");
-  static_assert(K::LDS >= (SORTED + 2) * 4, "the sequences' lengths pass through the same memory");
+  static_assert(K::LDS >= (2 * SORTED + 2) * 4, "the sequences' lengths pass through the same memory");
 
   const int tid = threadIdx.x;
   // Consecutive workgroups go to the XCDs in turn: each XCD has every eighth
@@ -604,11 +622,11 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   long row0;
   if (p.cu) {
     const int rows = p.segc ? p.segc * C : p.T + 1;
-    if (!packed_span<K::NT>(p, rows, place, reinterpret_cast<int*>(lds), sp.n, sp.seg)) return;
-    const int b = min(max(p.cu[sp.n], 0), p.T), e = min(max(p.cu[sp.n + 1], b), p.T);
-    row0 = b;
-    sp.len = e - b;
-    sp.slot = b / rows + sp.n + sp.seg;
+    if (!packed_span<PASS, K::NT>(p, rows, place, reinterpret_cast<int*>(lds), sp.n, sp.seg)) return;
+    const Rows r = rows_of(p, sp.n);
+    row0 = r.begin;
+    sp.len = r.len;
+    sp.slot = r.begin / rows + sp.seg;
   } else {
     sp.n = place / p.nseg;
     sp.seg = place % p.nseg;
@@ -665,42 +683,52 @@ int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, 
   return (int)best;
 }
 
-long segment_slots(int B, int T, bool packed, int segc, int chunk) {
+// Places of (sequence, segment) in a launch, by pass.
+long segment_places(int B, int T, bool packed, int segc, int chunk, int pass) {
   if (!segc) return B;
   const long rows = (long)segc * chunk;
-  return packed ? T / rows + B : B * (((long)T + rows - 1) / rows);
+  return packed ? T / rows + (pass == 0 ? B : 0) : B * (((long)T + rows - 1) / rows);
+}
+
+long workgroups(long places, const LinParams& p) {
+  return (places * p.H + 15) / 16 * 16 * p.nrole;  // whole groups on each of the eight XCDs
 }
 
 template <typename TI, int DX, int DZ>
-int launch_kernels(const LinParams& p, long wgs, hipStream_t s) {
-  if (p.segc) {
-    hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 1>), dim3((unsigned)wgs), dim3(LK<TI, DX, DZ, 1>::NT), 0, s, p);
+int launch_pass(LinParams p, hipStream_t s) {
+  const int chunk = LK<TI, DX, DZ, 0>::C;
+  const bool packed = p.cu != nullptr;
+  const long places[2] = {segment_places(p.B, p.T, packed, p.segc, chunk, 0),
+                          segment_places(p.B, p.T, packed, p.segc, chunk, 1)};
+  if (workgroups(places[0], p) >= 1L << 22) return GDN_ERR_INVALID_ARG;
+  p.nseg = p.segc && !packed ? (int)(places[0] / p.B) : 1;
+  if (p.segc && places[1] > 0) {
+    p.nslots = (int)places[1];
+    hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 1>), dim3((unsigned)workgroups(places[1], p)),
+                       dim3(LK<TI, DX, DZ, 1>::NT), 0, s, p);
     if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
   }
-  hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 0>), dim3((unsigned)wgs), dim3(LK<TI, DX, DZ, 0>::NT), 0, s, p);
+  p.nslots = (int)places[0];
+  hipLaunchKernelGGL((linear_kernel<TI, DX, DZ, 0>), dim3((unsigned)workgroups(places[0], p)),
+                     dim3(LK<TI, DX, DZ, 0>::NT), 0, s, p);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename TI, int DX>
-int launch_dz(const LinParams& p, int dz, long wgs, hipStream_t s) {
+int launch_dz(const LinParams& p, int dz, hipStream_t s) {
   switch (dz) {
-    case 32: return launch_kernels<TI, DX, 32>(p, wgs, s);
-    case 64: return launch_kernels<TI, DX, 64>(p, wgs, s);
-    default: return launch_kernels<TI, DX, 128>(p, wgs, s);
+    case 32: return launch_pass<TI, DX, 32>(p, s);
+    case 64: return launch_pass<TI, DX, 64>(p, s);
+    default: return launch_pass<TI, DX, 128>(p, s);
   }
 }
 
-int launch(LinParams p, int dx, int dz, int dtype, hipStream_t s) {
-  const long slots = segment_slots(p.B, p.T, p.cu != nullptr, p.segc, chunk_rows(dx, dz, dtype));
-  const long wgs = (slots * p.H + 15) / 16 * 16 * p.nrole;  // whole groups on each of the eight XCDs
-  if (wgs >= 1L << 22) return GDN_ERR_INVALID_ARG;
-  p.nslots = (int)slots;
-  p.nseg = p.segc && !p.cu ? (int)(slots / p.B) : 1;
+int launch(const LinParams& p, int dx, int dz, int dtype, hipStream_t s) {
   const bool b16 = dtype == GDN_BF16;
   switch (dx) {
-    case 32: return b16 ? launch_dz<__bf16, 32>(p, dz, wgs, s) : launch_dz<float, 32>(p, dz, wgs, s);
-    case 64: return b16 ? launch_dz<__bf16, 64>(p, dz, wgs, s) : launch_dz<float, 64>(p, dz, wgs, s);
-    default: return b16 ? launch_dz<__bf16, 128>(p, dz, wgs, s) : launch_dz<float, 128>(p, dz, wgs, s);
+    case 32: return b16 ? launch_dz<__bf16, 32>(p, dz, s) : launch_dz<float, 32>(p, dz, s);
+    case 64: return b16 ? launch_dz<__bf16, 64>(p, dz, s) : launch_dz<float, 64>(p, dz, s);
+    default: return b16 ? launch_dz<__bf16, 128>(p, dz, s) : launch_dz<float, 128>(p, dz, s);
   }
 }
 
@@ -725,7 +753,7 @@ struct Plan {
 Plan plan(int B, int T, int H, int dx, int dz, int roles, bool packed, int dtype) {
   const int segc = segment_chunks(B, T, H, dx, dz, roles, packed, dtype);
   if (!segc) return {0, 0};
-  return {segc, segment_slots(B, T, packed, segc, chunk_rows(dx, dz, dtype)) * H * roles * dx * dz * 4LL};
+  return {segc, segment_places(B, T, packed, segc, chunk_rows(dx, dz, dtype), 1) * H * roles * dx * dz * 4LL};
 }
 
 }  // namespace

@@ -241,7 +241,10 @@ def linear_attention(q, k, v, g, h0=None, cu_seqlens=None):
     """(out, hT) of ``linear_fwd`` as a differentiable torch operation:
     gradients for q, k, v and h0 through ``linear_bwd``.  Arguments as for
     ``linear_fwd``.  With packed sequences that leave rows out, those rows'
-    outputs and gradients are zero."""
+    outputs and gradients are zero.  To capture a training step into a graph,
+    call ``linear_fwd`` and ``linear_bwd`` themselves: autograd's own
+    accumulation into leaves that an eager graph still holds waits for
+    another stream, which a capture does not survive."""
     global _LINEAR
     if _LINEAR is None:
         import torch

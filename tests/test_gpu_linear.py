@@ -374,12 +374,13 @@ def test_no_tokens(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B", [511, 700])
+@pytest.mark.parametrize("B", [64, 65, 700])
 def test_many_packed_sequences(dtype, B):
-    """More sequences than are put in order of length, and just fewer; some long enough to be cut."""
+    """As many sequences as are put in order of length, and more; some long enough to be cut, some a whole
+    number of segments."""
     r = np.random.default_rng(B)
     lens = r.integers(0, 5, B)
-    lens[[3, B // 2, B - 1]] = [400, 333, 129]
+    lens[[3, 11, B // 2, B - 1]] = [400, 256, 333, 128]
     bounds = [0, *np.cumsum(lens).tolist()]
     c = make(B, dtype, bounds[-1], 1, 32, 32, B, packed=True, slow=True)
     check(run_all(c, torch.tensor(bounds, dtype=torch.int32, device="cuda")), c, dtype, bounds)

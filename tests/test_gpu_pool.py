@@ -106,6 +106,14 @@ def test_batches(delta, B, H):
 
 
 @pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(32, 64), (32, 128), (64, 128), (128, 64), (128, 128)])
+def test_many_chains(delta, dtype, dk, dv):
+    """Enough chains that one workgroup takes all of a chain's columns."""
+    check(make(dk + 7 * dv, dtype, 90, 2, 3, dk, dv, 91), delta)
+
+
+@pytest.mark.parametrize("delta", [False, True])
 def test_slots_of_no_sequence(delta):
     """Padding rows, slots outside the pool, and a slot named again: no state changes, zeros come out."""
     c = make(1, "bf16", 8, 2, 2, 64, 128, 6)

@@ -116,6 +116,9 @@ def test_workspace():
     assert need > 0 and need % (2 * 128 * 128 * 4) == 0
     assert size(3, 32768, 2, 128, 128, 1, 1) > 0
     assert size(1, 32768, 2, 128, 64, 0, 1, 1) > 0
+    # however many sequences: about as many segment states as the device has compute units
+    for B in (1, 100, 5000):
+        assert 0 <= size(B, 200000, 16, 128, 128, 1, 1) <= 256 * 128 * 128 * 4
     for packed in (0, 1):
         for backward in (0, 1):  # no rows, no sequences
             assert size(3, 0, 2, 128, 64, packed, 1, backward) == 0
