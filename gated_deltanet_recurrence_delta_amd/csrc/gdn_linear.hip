@@ -93,8 +93,10 @@ struct LK {
   // scores.
   static constexpr int YB = C * DX * ES, ZB = C * DZ * ES, AT_Y = PASS == 0 ? YB : 0, AT_Z = AT_Y + YB, SB = AT_Z + ZB;
   static constexpr int NBUF = PASS == 0 ? 3 : 4;
-  // bf16 terms that the decayed z are taken as where they enter the state
-  static constexpr int TERMS = !B16 ? 1 : (PASS == 0 ? 3 : 2);
+  // bf16 terms that the decayed z are taken as where they enter the state:
+  // their 24 bits (two terms would leave 2^-18 of each value, and spare 2% of
+  // a pass that memory bounds)
+  static constexpr int TERMS = B16 ? 3 : 1;
   // Fragments of scores, rows 16 ib and on against SLAB columns from SLAB js on.
   __host__ __device__ static constexpr int frag_at(int ib, int js) {
     int n = js;
@@ -357,7 +359,7 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   // A chunk's z columns as fragments over the rows (for two 16-row blocks:
   // rows 4 q4 and on of the first, then of the second, as the scores'
   // accumulators lie), and as they enter the state: decayed, in 16-bit
-  // storage as TERMS terms (three are their 24 bits in full).
+  // storage as TERMS terms.
   struct ZCols {
     Frag f[K::NJS], t[K::NJS][K::TERMS];
   };

@@ -9,10 +9,10 @@ to a term of a sum moves the sum by at most r A:
   within 2^-24;
 - bf16: the masked scores or the state, and (for the outputs) the products'
   other operand being exact, one rounding of 2^-8 A, and the output's own
-  2^-8 |out|; values that enter the state are kept as two bf16 terms,
-  2^-16 A.
+  2^-8 |out|; values that enter the state keep 16 bits at least, 2^-16 A.
 
-The decays' two terms leave 2^-48 a chunk, below all of these.
+A decay near one is applied as m + (a^n - 1) m, in one rounding: no factor's own
+rounding adds up over the chunks.
 """
 import numpy as np
 import pytest

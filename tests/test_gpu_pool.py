@@ -296,7 +296,7 @@ def test_serving_run(dtype):
                 q, k, v = (f64(x)[None] for x in h)
                 o, S = linear.fwd(q, k, v, f64(g))
                 mo, mS = linear.fwd(np.abs(q), np.abs(k), np.abs(v), f64(g))
-                # the prompt's chunks (bf16: values as two terms), then the tokens, each with its own sums
+                # the prompt's chunks (bf16: values of 16 bits at least), then the tokens, each with its own sums
                 n = (2.0 ** -16 if dtype == "bf16" else 0) + (64 + 64 + 4 * 4 + 3 * 8 + 20) * 2.0 ** -24
                 e = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
                 assert (np.abs(f64(out[i, 0]) - o[0, -1]) <= n * mo[0, -1] + e * (np.abs(o[0, -1]) + n * mo[0, -1])).all()

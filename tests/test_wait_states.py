@@ -75,8 +75,8 @@ def early_readers(text):
     return bad, products
 
 
-def test_checker():
-    """The check sees an early reader behind a branch, and no other."""
+def test_an_early_reader_is_seen():
+    """Behind a branch, and no other."""
     text = """
 f:                                      ; @f
 	v_mfma_f32_16x16x4_f32 v[0:3], v8, v9, v[0:3]
