@@ -103,7 +103,10 @@ struct LK {
     for (int i = 0; i < ib; ++i) n += i / TPS + 1;
     return n;
   }
-  static constexpr int NFR = frag_at(NB, 0), PB = PASS == 0 ? NFR * 1024 : 0, DB = PASS == 0 ? 2048 : 0;
+  // In bf16 they are two terms, 16 bits: with the state's and the outputs' own
+  // roundings a third one would show, and two more products a chunk do not.
+  static constexpr int PT = B16 ? 2 : 1, NFR = PT * frag_at(NB, 0);
+  static constexpr int PB = PASS == 0 ? NFR * 1024 : 0, DB = PASS == 0 ? 2048 : 0;
   static constexpr int AT_P = NBUF * SB, AT_D = AT_P + 2 * PB, LDS = AT_D + DB;
   static constexpr int Y_INS = YB / 1024, Z_INS = ZB / 1024;  // copies of 1 KB
   static constexpr int GROUP = (DX < DZ ? DX : DZ) * ES < 128 ? 2 : 1;  // heads whose rows share a 128-byte line
@@ -332,9 +335,14 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       const f32x4 decay = lds_ld<f32x4>(sD, ((ib - jb) * 64 + lane) * 16);
 #pragma unroll
       for (int e = 0; e < 4; ++e) P[e] *= decay[e];
-      char* at = to + (K::frag_at(ib, jb / K::TPS) * 64 + lane) * 16;
-      if constexpr (K::B16) lds_st(at, 8 * (jb & 1), cvt4(P));
-      else lds_st(at, 0, P);
+      char* at = to + (K::PT * K::frag_at(ib, jb / K::TPS) * 64 + lane) * 16;
+      if constexpr (K::B16) {
+        const u32x2 first = __builtin_bit_cast(u32x2, cvt4(P));
+        lds_st(at, 8 * (jb & 1), first);
+        lds_st(at, 1024 + 8 * (jb & 1), cvt4(left_over(P, first)));
+      } else {
+        lds_st(at, 0, P);
+      }
     };
     constexpr int BLOCKS = K::NB * (K::NB + 1) / 2;
 #pragma unroll
@@ -448,7 +456,9 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       for (int ib = 0; ib < K::NB; ++ib) {
 #pragma unroll
         for (int js = 0; js * K::TPS <= ib; ++js)
-          O[ib] = Mma<TI>::mma(z.f[js], lds_ld<Frag>(bP, (K::frag_at(ib, js) * 64 + lane) * 16), O[ib]);
+#pragma unroll
+          for (int t = K::PT - 1; t >= 0; --t)
+            O[ib] = Mma<TI>::mma(z.f[js], lds_ld<Frag>(bP, ((K::PT * K::frag_at(ib, js) + t) * 64 + lane) * 16), O[ib]);
         if constexpr (K::B16)
           __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, cvt4(O[ib])), ro, (int)(o_off + ib * o_blk), 0,
                                                 0);

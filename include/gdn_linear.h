@@ -72,9 +72,9 @@ extern "C" {
  * nothing is cut.
  *
  * Arithmetic: GDN_BF16: every product on the bf16 matrix cores with fp32
- * accumulation; the masked scores and the state are rounded to bf16 as
- * operands of the outputs only, and the decayed values that enter the state
- * are taken as three bf16 terms, all of their 24 bits.  GDN_F32: fp32
+ * accumulation; the state is rounded to bf16 as an operand of the outputs
+ * only, the masked scores are taken as two bf16 terms (16 bits), and the
+ * decayed values that enter the state as three, all of their 24 bits.  GDN_F32: fp32
  * throughout.  The state is carried in fp32 in both, and a constant decay's rounding does not add up
  * over a long sequence.  Non-finite inputs propagate within their own head
  * and sequence, to the rows of the same chunk (32 rows at most) before them
