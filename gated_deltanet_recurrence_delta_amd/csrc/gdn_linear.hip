@@ -70,7 +70,7 @@ struct LinParams {
   const int32_t* cu;  // null: dense
   f32x4* ws;          // end states of the segments
   int B, T, H, nrole;
-  int segc;           // chunks of a segment; 0: nothing is cut
+  int segc;           // chunks of a segment, an even number; 0: nothing is cut
   int nslots;         // places of (sequence, segment)
   int nseg;           // of them a dense sequence's
 };
@@ -85,7 +85,10 @@ struct LK {
   // which leaves room for two workgroups on a CU (dx = 128, dz = 32, 512
   // chains of 4,096 rows: 594 us, with 32 rows 1,089), but 32 at 128 x 128,
   // where there is room for one either way (700 us against 766).
-  static constexpr int C = B16 || (DX == 128 && DZ == 128) ? 32 : 16, NB = C / 16;
+  // The end states of segments, which need no scores, take twice the rows in
+  // bf16: half the decays of the state.
+  static constexpr int UNIT = B16 || (DX == 128 && DZ == 128) ? 32 : 16;  // of segments
+  static constexpr int C = UNIT * (PASS == 1 && B16 ? 2 : 1), NB = C / 16;
   static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
   static constexpr int GR = DX * ES / 16, ZGR = DZ * ES / 16;  // 16-byte granules of a row
   static constexpr int NS = DX / SLAB, NJS = C / SLAB, TPS = SLAB / 16, NU = DX / 16;
@@ -280,8 +283,8 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
       }
     }
   } else if (PASS == 0) {
-    const Decay a = decay_of(pow_of(gh, (long)p.segc * C));
-    const double nats = -(double)gh * p.segc * C;
+    const Decay a = decay_of(pow_of(gh, (long)p.segc * K::UNIT));
+    const double nats = -(double)gh * p.segc * K::UNIT;
     const int first = nats * sp.seg > FORGOTTEN ? max(sp.slot - sp.seg, sp.slot - 1 - (int)(FORGOTTEN / nats))
                                                 : sp.slot - sp.seg;
     for (int s = first; s < sp.slot; ++s) {
@@ -331,7 +334,7 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
 #pragma unroll
       for (int s = 0; s < K::NS; ++s)
         P = Mma<TI>::mma(lds_ld<Frag>(bY, x_row + x_granule(s)), lds_ld<Frag>(bX, x_row + x_granule(s)), P);
-      static_assert(K::NB <= 2, "two tables of decays");
+      static_assert(PASS == 1 || K::NB <= 2, "two tables of decays");
       const f32x4 decay = lds_ld<f32x4>(sD, ((ib - jb) * 64 + lane) * 16);
 #pragma unroll
       for (int e = 0; e < 4; ++e) P[e] *= decay[e];
@@ -633,7 +636,7 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   sp.h = chain % p.H;
   long row0;
   if (p.cu) {
-    const int rows = p.segc ? p.segc * C : p.T + 1;
+    const int rows = p.segc ? p.segc * K::UNIT : p.T + 1;
     if (!packed_span<PASS, K::NT>(p, rows, place, reinterpret_cast<int*>(lds), sp.n, sp.seg)) return;
     const Rows r = rows_of(p, sp.n);
     row0 = r.begin;
@@ -648,8 +651,9 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   }
   sp.th0 = row0 * p.H + sp.h;
   sp.nch = (sp.len + C - 1) / C;
-  sp.c0 = sp.seg * p.segc;
-  sp.c1 = p.segc ? min(sp.nch, sp.c0 + p.segc) : sp.nch;
+  const int segc = p.segc / (C / K::UNIT);  // whole: segments have an even number of units
+  sp.c0 = sp.seg * segc;
+  sp.c1 = segc ? min(sp.nch, sp.c0 + segc) : sp.nch;
   if (sp.seg > 0 && sp.c0 >= sp.nch) return;
   const float gh = p.g[sp.h];
   if constexpr (PASS == 1) {
@@ -666,7 +670,7 @@ constexpr int CUS = 256;    // of an MI355X
 constexpr int SEG_MIN = 4;  // chunks a segment has at least
 constexpr int PACKED_SEG_MIN = 4;
 
-int chunk_rows(int dx, int dz, int dtype) { return dtype == GDN_BF16 || (dx == 128 && dz == 128) ? 32 : 16; }  // LK::C
+int chunk_rows(int dx, int dz, int dtype) { return dtype == GDN_BF16 || (dx == 128 && dz == 128) ? 32 : 16; }  // LK::UNIT
 
 // Chunks of a segment, or 0: a sequence is cut where a batch has fewer
 // chains than the device holds workgroups.  What a cut costs is a first
@@ -678,18 +682,18 @@ int segment_chunks(int B, int T, int H, int dx, int dz, int roles, bool packed, 
   if (packed) {
     // lengths are not known here: no segment is longer than an even share
     const long all = ((long)T + rows - 1) / rows;
-    const long share = std::max<long>(PACKED_SEG_MIN, (all * H * roles + room - 1) / room);
+    const long share = (std::max<long>(PACKED_SEG_MIN, (all * H * roles + room - 1) / room) + 1) / 2 * 2;
     return share < all ? (int)share : 0;
   }
   const long nch = ((long)T + rows - 1) / rows;
   long best = 0, least = 0;
   for (long n = 1; n <= 32 && (n == 1 || nch / n >= SEG_MIN); ++n) {
-    const long segc = (nch + n - 1) / n, segs = (nch + segc - 1) / segc;
+    const long segc = ((nch + n - 1) / n + 1) / 2 * 2, segs = (nch + segc - 1) / segc;  // an even number
     long cost = 10 * ((chains * segs + room - 1) / room) * (segc + 1);
     if (n > 1) cost += 6 * ((chains * (segs - 1) + room - 1) / room) * (segc + 1) + 20;
     if (n == 1 || cost < least) {
       least = cost;
-      best = n == 1 ? 0 : segc;
+      best = segs == 1 ? 0 : segc;
     }
   }
   return (int)best;
@@ -708,7 +712,7 @@ long workgroups(long places, const LinParams& p) {
 
 template <typename TI, int DX, int DZ>
 int launch_pass(LinParams p, hipStream_t s) {
-  const int chunk = LK<TI, DX, DZ, 0>::C;
+  const int chunk = LK<TI, DX, DZ, 0>::UNIT;
   const bool packed = p.cu != nullptr;
   const long places[2] = {segment_places(p.B, p.T, packed, p.segc, chunk, 0),
                           segment_places(p.B, p.T, packed, p.segc, chunk, 1)};
