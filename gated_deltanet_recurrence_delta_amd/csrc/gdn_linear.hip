@@ -30,7 +30,7 @@
 //
 // Bound by memory: every row is read once by one workgroup, or twice where
 // its chain is cut (two launches, see segment_chunks).  B=4 H=16 T=4096,
-// dx = dz = 128 bf16: 37 us for the segments' states, 61 us for the outputs,
+// dx = dz = 128 bf16: 39 us for the segments' states, 61 us for the outputs,
 // 64 KB for each 64 rows of a workgroup in 3.2 us, 5.1 TB/s over the device (a
 // copy of the same size reaches 4.7); 11 us of each launch are its start, the
 // first chunks' way and the last stores.  512 chains uncut (2.1 GB): 479 us,
@@ -86,7 +86,8 @@ struct LK {
   // chains of 4,096 rows: 594 us, with 32 rows 1,089), but 32 at 128 x 128,
   // where there is room for one either way (700 us against 766).
   // The end states of segments, which need no scores, take twice the rows in
-  // bf16: half the decays of the state.
+  // bf16: half the decays of the state (32,768 rows of 16 heads at 128 x 128:
+  // 184 us, with 32 rows in both 199).
   static constexpr int UNIT = B16 || (DX == 128 && DZ == 128) ? 32 : 16;  // of segments
   static constexpr int C = UNIT * (PASS == 1 && B16 ? 2 : 1), NB = C / 16;
   static constexpr int NW = DZ / 16, NT = 64 * NW;             // waves, threads
