@@ -50,6 +50,7 @@
 #include "gdn_checks.h"
 #include "gdn_device.h"
 #include "gdn_linear.h"
+#include "gdn_linear_places.h"
 
 namespace {
 
@@ -542,73 +543,22 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
   }
 }
 
-// The begin and length of a packed batch's sequence, within the rows there are.
-struct Rows {
-  int begin, len;
-};
-__device__ static inline Rows rows_of(const LinParams& p, int i) {
-  const int b = min(max(p.cu[i], 0), p.T);
-  return {b, min(max(p.cu[i + 1], b), p.T) - b};
-}
-
-constexpr int SORTED = 64;  // sequences of a packed batch that are put in order of length
-
-// The (sequence, segment) that comes at place `at` of a packed batch cut into
-// segments of `rows` rows; false: there is none.
-//
-// PASS 1 goes by the slots of the segments that others follow: a sequence's
-// are floor(begin / rows) and on, as many as whole segments fit in it at most,
-// so that the sequences' slots are apart and below floor(T / rows).
-//
-// PASS 0 takes whole segments first and then the sequences' last ones from
-// long to short, so that the workgroups that start late are short ones
-// (64,711 rows in 32 sequences of 16 heads, dx = dz = 128: 252 us, in the
-// order of the batch 338).  With more sequences the order matters less and
-// costs more (50,000 rows in 100: 232 against 225), and sequence i has the
-// places floor(begin / rows) + i and on.
+// The place of a workgroup in a packed batch (one for all of its threads:
+// what follows from it stays in scalar registers).
 template <int PASS, int NT>
-__device__ static inline bool packed_span(const LinParams& p, int rows, int at, int* lds, int& n, int& seg) {
+__device__ static inline Place packed_place(const Packed& b, int rows, int at, PlaceBoard& board) {
   const int tid = threadIdx.x;
-  int *found = lds, *whole = lds + 2, *rest = whole + SORTED;
-  if (tid == 0) found[0] = -1;
-  if (PASS == 0 && p.B <= SORTED) {
-    for (int i = tid; i < p.B; i += NT) {
-      const int len = rows_of(p, i).len;
-      whole[i] = len / rows;
-      rest[i] = len % rows > 0 || len == 0 ? len % rows : -1;  // -1: whole segments alone
-    }
-    __syncthreads();
-    for (int i = tid; i < p.B; i += NT) {
-      const int wi = whole[i], ri = rest[i];
-      int before = 0, all = 0, longer = 0;
-      for (int j = 0; j < p.B; ++j) {
-        const int wj = whole[j], rj = rest[j];
-        all += wj;
-        before += j < i ? wj : 0;
-        longer += rj > ri || (rj == ri && j < i);
-      }
-      if (at < all ? at >= before && at < before + wi : ri >= 0 && at - all == longer) {
-        found[0] = i;
-        found[1] = at < all ? at - before : wi;
-      }
-    }
-  } else {
-    __syncthreads();
-    for (int i = tid; i < p.B; i += NT) {
-      const Rows r = rows_of(p, i);
-      const int segs = (r.len + rows - 1) / rows;
-      const int first = r.begin / rows + (PASS == 0 ? i : 0), count = PASS == 0 ? max(1, segs) : segs - 1;
-      if (at >= first && at < first + count) {
-        found[0] = i;
-        found[1] = at - first;
-      }
-    }
-  }
+  const Places<PASS> places = {b, rows, at};
+  places.begin(tid, board);
   __syncthreads();
-  n = __builtin_amdgcn_readfirstlane(found[0]);  // one for all: what follows from it stays in scalar registers
-  seg = __builtin_amdgcn_readfirstlane(found[1]);
+  places.look(tid, NT, board);
   __syncthreads();
-  return n >= 0;
+  places.settle(tid, NT, board);
+  __syncthreads();
+  const Place r = places.place(board);
+  __syncthreads();
+  return {__builtin_amdgcn_readfirstlane(r.n), __builtin_amdgcn_readfirstlane(r.seg),
+          __builtin_amdgcn_readfirstlane(r.uncut) != 0};
 }
 
 // PASS 0: outputs (and end states); PASS 1: the end states of the segments
@@ -621,7 +571,7 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   __shared__ double sPow[C + 1];
   __shared__ float sIn[2 * C];  // the decay's powers from C down to 0, then zeros
   static_assert(K::NT >= 2 * C, "a thread for each");
-  static_assert(K::LDS >= (2 * SORTED + 2) * 4, "the sequences' lengths pass through the same memory");
+  static_assert(K::LDS >= (int)sizeof(PlaceBoard), "the board is in the same memory");
 
   const int tid = threadIdx.x;
   // Consecutive workgroups go to the XCDs in turn: each XCD has every eighth
@@ -636,11 +586,17 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   const int place = chain / p.H;
   sp.h = chain % p.H;
   long row0;
+  bool cut = p.segc != 0;
   if (p.cu) {
-    const int rows = p.segc ? p.segc * K::UNIT : p.T + 1;
-    if (!packed_span<PASS, K::NT>(p, rows, place, reinterpret_cast<int*>(lds), sp.n, sp.seg)) return;
-    const Rows r = rows_of(p, sp.n);
+    const int rows = cut ? p.segc * K::UNIT : p.T + 1;
+    const Packed batch = {p.cu, p.B, p.T};
+    const Place at = packed_place<PASS, K::NT>(batch, rows, place, *reinterpret_cast<PlaceBoard*>(lds));
+    if (at.n < 0) return;
+    const Rows r = rows_of(batch, at.n);
+    cut = cut && !at.uncut;
     row0 = r.begin;
+    sp.n = at.n;
+    sp.seg = at.seg;
     sp.len = r.len;
     sp.slot = r.begin / rows + sp.seg;
   } else {
@@ -654,7 +610,7 @@ __global__ __launch_bounds__((LK<TI, DX, DZ, PASS>::NT), 2) void linear_kernel(c
   sp.nch = (sp.len + C - 1) / C;
   const int segc = p.segc / (C / K::UNIT);  // whole: segments have an even number of units
   sp.c0 = sp.seg * segc;
-  sp.c1 = segc ? min(sp.nch, sp.c0 + segc) : sp.nch;
+  sp.c1 = cut ? min(sp.nch, sp.c0 + segc) : sp.nch;
   if (sp.seg > 0 && sp.c0 >= sp.nch) return;
   const float gh = p.g[sp.h];
   if constexpr (PASS == 1) {

@@ -36,8 +36,11 @@ extern "C" {
  *   number of rows, cu_seqlens a DEVICE int32 array of B+1 offsets; sequence
  *   n is rows [cu_seqlens[n], cu_seqlens[n+1]), an independent recurrence.
  *   Offsets are taken into [0, T] and an end before its begin is an empty
- *   sequence, so no offset reads or writes outside the tensors; sequences
- *   that overlap race on out.  Rows of no sequence are left as they were.
+ *   sequence, so no offset reads or writes outside the tensors.  Every
+ *   sequence has its own rows and state whatever the offsets' order, but where
+ *   one lies before an earlier one nothing is cut into segments (see below),
+ *   and sequences that overlap race on out (not on hT).  Rows of no sequence
+ *   are left as they were.
  * State, both modes: h0 (B, H, dk, dv) float32 or NULL (zero); hT the same
  *   shape, written; hT may be h0 itself (not a part of it).  A sequence of
  *   length 0 gets hT = h0 (or zeros).
