@@ -19,11 +19,10 @@
 
 #include <algorithm>
 #include <new>
-#include <utility>
-#include <vector>
 
 #include "gdn_checks.h"
 #include "gdn_linear.h"
+#include "gdn_move_plan.h"
 #include "gdn_pool.h"
 
 namespace {
@@ -299,30 +298,14 @@ int recurrent(const void* q, const void* k, const void* v, const float* g, const
 
 // ------------------------------------------------------------ moving slots --
 //
-// Every pair writes a slot that no other pair writes, and reads one that may
-// be written by another.  Put in an order in which each slot is read before
-// it is written, the pairs can run one after the other with no second copy of
-// anything: pairs whose target nobody reads come first, and each makes its
-// source one reader poorer.  What is left then are plain cycles; one of a
-// cycle's slots is kept in registers.  Pairs that neither read what another
-// writes nor the other way round are in groups of their own and run side by
-// side.  A thread carries the same bytes of every slot of its group through
-// the whole list, so the order needs no barrier, and since no slot is written
+// The pairs are put in an order that needs no second copy (gdn_move_plan.h).
+// A thread carries the same bytes of every slot of its group through the
+// whole list, so the order needs no barrier, and since no slot is written
 // before its last reading the loads of several steps can be on their way at
 // once.  Bound by memory: one read of each source, one write of each target.
 
-constexpr int MAX_STEPS = 320;  // steps of one launch: the list travels as kernel arguments (4 KB at most)
-constexpr int STEP_ZERO = -1;   // source: zeros
-constexpr int STEP_KEPT = -2;   // source: the registers that a cycle's first slot was kept in; target: keep it there
-constexpr int FAN = 8;          // targets that one group takes from one source with a single reading
 constexpr int MOVE_NT = 256;
 constexpr int MOVE_V = 4;       // 16-byte pieces a thread carries
-
-struct MoveList {
-  int src[MAX_STEPS];
-  int dst[MAX_STEPS];
-  uint16_t begin[MAX_STEPS + 1];
-};
 
 __global__ __launch_bounds__(MOVE_NT) void move_kernel(f4* __restrict__ pool, const long pieces, const long slots,
                                                       const MoveList m) {
@@ -358,153 +341,19 @@ __global__ __launch_bounds__(MOVE_NT) void move_kernel(f4* __restrict__ pool, co
   }
 }
 
-struct Mover {
-  f4* pool;
-  long long outer, slots, pieces;
-  hipStream_t stream;
-  MoveList list;
-  int steps = 0, groups = 0;
-  std::vector<std::pair<MoveList, int>> launches;  // all planned before the first is queued
-
-  void flush() {
-    if (groups) {
-      list.begin[groups] = (uint16_t)steps;
-      launches.emplace_back(list, groups);
-    }
-    steps = groups = 0;
-  }
-  int run() const {
-    const unsigned tiles = (unsigned)((pieces + MOVE_NT * MOVE_V - 1) / (MOVE_NT * MOVE_V));
-    for (const auto& l : launches)
-      for (long long o = 0; o < outer; o += 65535) {
-        const unsigned z = (unsigned)std::min<long long>(65535, outer - o);
-        hipLaunchKernelGGL(move_kernel, dim3(tiles, l.second, z), dim3(MOVE_NT), 0, stream,
-                           pool + o * slots * pieces, (long)pieces, (long)slots, l.first);
-        if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
-      }
-    return GDN_OK;
-  }
-  // One group, steps in order; a group longer than a launch goes on in the
-  // next one, behind it on the stream.
-  void add(const std::vector<std::pair<int, int>>& g) {
-    size_t i = 0;
-    while (i < g.size()) {
-      const size_t room = MAX_STEPS - steps;
-      if (g.size() - i > room && (i > 0 || g.size() <= MAX_STEPS) && steps > 0) {
-        flush();
-        continue;
-      }
-      const size_t n = std::min(room, g.size() - i);
-      list.begin[groups++] = (uint16_t)steps;
-      for (size_t j = 0; j < n; ++j, ++steps) {
-        list.src[steps] = g[i + j].first;
-        list.dst[steps] = g[i + j].second;
-      }
-      i += n;
-      if (i < g.size()) flush();
-    }
-  }
-};
-
 int move_slots(f4* pool, long long outer, long long slots, long long pieces, const int32_t* src, const int32_t* dst,
                int n, hipStream_t stream) {
-  // (target, source), sorted by target: the writer of a slot is found by bisection
-  std::vector<std::pair<int, int>> w;
-  w.reserve(n);
-  for (int i = 0; i < n; ++i) {
-    if (dst[i] < 0 || dst[i] >= slots || src[i] < -1 || src[i] >= slots) return GDN_ERR_INVALID_ARG;
-    w.emplace_back(dst[i], src[i]);
-  }
-  std::sort(w.begin(), w.end());
-  for (int i = 1; i < n; ++i)
-    if (w[i].first == w[i - 1].first) return GDN_ERR_INVALID_ARG;
-  w.erase(std::remove_if(w.begin(), w.end(), [](const std::pair<int, int>& p) { return p.first == p.second; }),
-          w.end());
-  if (w.empty() || outer == 0) return GDN_OK;
-  n = (int)w.size();
-  std::vector<int> writer(n, -1), readers(n, 0), up(n);  // pair -> pair that writes its source; how many read its target
-  for (int i = 0; i < n; ++i) {
-    up[i] = i;
-    if (w[i].second < 0) continue;
-    const auto it = std::lower_bound(w.begin(), w.end(), std::make_pair(w[i].second, INT32_MIN));
-    if (it != w.end() && it->first == w[i].second) {
-      writer[i] = (int)(it - w.begin());
-      ++readers[writer[i]];
+  MovePlan plan;  // whole before its first launch is queued
+  if (!plan_moves(plan, slots, src, dst, n)) return GDN_ERR_INVALID_ARG;
+  const unsigned tiles = (unsigned)((pieces + MOVE_NT * MOVE_V - 1) / (MOVE_NT * MOVE_V));
+  for (const auto& l : plan.launches)
+    for (long long o = 0; o < outer; o += 65535) {
+      const unsigned z = (unsigned)std::min<long long>(65535, outer - o);
+      hipLaunchKernelGGL(move_kernel, dim3(tiles, l.second, z), dim3(MOVE_NT), 0, stream, pool + o * slots * pieces,
+                         (long)pieces, (long)slots, l.first);
+      if (hipGetLastError() != hipSuccess) return GDN_ERR_LAUNCH;
     }
-  }
-  Mover mv{pool, outer, slots, pieces, stream, {}, 0, 0, {}};
-  std::vector<std::pair<int, int>> g;
-  // 1. pairs that no other pair has to wait for or be waited for, those of one source together
-  std::vector<std::pair<int, int>> alone;
-  for (int i = 0; i < n; ++i)
-    if (writer[i] < 0 && readers[i] == 0) alone.emplace_back(w[i].second, w[i].first);
-  std::sort(alone.begin(), alone.end());
-  for (size_t i = 0; i < alone.size(); ++i) {
-    if (!g.empty() && (g.back().first != alone[i].first || g.size() == FAN)) {
-      mv.add(g);
-      g.clear();
-    }
-    g.push_back(alone[i]);
-  }
-  if (!g.empty()) mv.add(g);
-  // 2. the others, by connected component
-  auto root = [&](int i) {
-    while (up[i] != i) i = up[i] = up[up[i]];
-    return i;
-  };
-  for (int i = 0; i < n; ++i)
-    if (writer[i] >= 0) up[root(i)] = root(writer[i]);
-  std::vector<std::pair<int, int>> of;  // (component, pair)
-  for (int i = 0; i < n; ++i)
-    if (writer[i] >= 0 || readers[i] > 0) of.emplace_back(root(i), i);
-  std::sort(of.begin(), of.end());
-  std::vector<std::pair<int, int>> ready;  // (source, pair)
-  std::vector<char> done(n, 0);
-  for (size_t b = 0; b < of.size();) {
-    size_t e = b;
-    while (e < of.size() && of[e].first == of[b].first) ++e;
-    g.clear();
-    ready.clear();
-    for (size_t i = b; i < e; ++i)
-      if (readers[of[i].second] == 0) ready.emplace_back(w[of[i].second].second, of[i].second);
-    std::sort(ready.begin(), ready.end());
-    while (!ready.empty()) {
-      const int i = ready.back().second;
-      ready.pop_back();
-      done[i] = 1;
-      g.emplace_back(w[i].second, w[i].first);
-      const int up_ = writer[i];
-      if (up_ >= 0 && --readers[up_] == 0) ready.emplace_back(w[up_].second, up_);
-    }
-    // What is left is at most one cycle.  A long one is turned in pieces:
-    // turning a_0 .. a_k first leaves a_0's old state in a_k, and the rest,
-    // a_k among it, is a shorter cycle.
-    for (size_t i = b; i < e; ++i) {
-      int at = of[i].second;
-      if (done[at]) continue;
-      std::vector<int> cyc;
-      for (; !done[at]; at = writer[at]) {
-        done[at] = 1;
-        cyc.push_back(w[at].first);
-      }
-      for (size_t s = 0; s + 1 < cyc.size();) {
-        const size_t k = std::min(cyc.size(), s + (size_t)MAX_STEPS - 2);
-        if (s > 0 || g.size() + (k - s) + 1 > (size_t)MAX_STEPS) {  // a piece of a cycle stays in one launch
-          mv.add(g);
-          mv.flush();
-          g.clear();
-        }
-        g.emplace_back(cyc[s], STEP_KEPT);
-        for (size_t j = s; j + 1 < k; ++j) g.emplace_back(cyc[j + 1], cyc[j]);
-        g.emplace_back(STEP_KEPT, cyc[k - 1]);
-        s = k - 1;
-      }
-    }
-    mv.add(g);
-    b = e;
-  }
-  mv.flush();
-  return mv.run();
+  return GDN_OK;
 }
 
 }  // namespace
