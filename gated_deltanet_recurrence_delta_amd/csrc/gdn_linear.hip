@@ -289,12 +289,25 @@ __device__ static inline void compute(const LinParams& p, const Span& sp, const 
     const double nats = -(double)gh * p.segc * K::UNIT;
     const int first = nats * sp.seg > FORGOTTEN ? max(sp.slot - sp.seg, sp.slot - 1 - (int)(FORGOTTEN / nats))
                                                 : sp.slot - sp.seg;
-    for (int s = first; s < sp.slot; ++s) {
+    auto add = [&](int s) {
       const f32x4* src = ws_at(s);
-      if (a.near_one) apply<true>(a.f, M);
-      else apply<false>(a.f, M);
 #pragma unroll
       for (int u = 0; u < K::NU; ++u) M[u] += src[u * 64];
+    };
+    if (a.near_one && __builtin_isinf(a.f)) {
+      // A growing state may be zero in segments over which the growth is past
+      // fp32: it grows chunk by chunk, and zeros stay zeros.
+      const float f = (float)(sPow[C] - 1.0);
+      for (int s = first; s < sp.slot; ++s) {
+        for (int c = 0; c < p.segc; ++c) apply<true>(f, M);
+        add(s);
+      }
+    } else {
+      for (int s = first; s < sp.slot; ++s) {
+        if (a.near_one) apply<true>(a.f, M);
+        else apply<false>(a.f, M);
+        add(s);
+      }
     }
   }
 

@@ -81,8 +81,8 @@ extern "C" {
  * throughout.  The state is carried in fp32 in both, and a constant decay's rounding does not add up
  * over a long sequence.  Non-finite inputs propagate within their own head
  * and sequence, to the rows of the same chunk (32 rows at most) before them
- * too.  A positive g is computed as it stands, as long as the powers over 32
- * rows are finite.
+ * too.  A positive g is computed as it stands, as long as the decay over 64
+ * rows, exp(64 g), is finite in fp32 and the states are.
  */
 int gdn_linear_fwd(const void* q, const void* k, const void* v, const float* g,
                    const float* h0, const int32_t* cu_seqlens, void* out,
