@@ -180,7 +180,8 @@ def linear_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None, stream=N
     q, k: (B,T,H,dk); v: (B,T,H,dv), one dtype, float32 or bfloat16; g: (H,)
     float32, the natural logarithm of each head's decay, <= 0 (packed: drop B
     and pass int32 ``cu_seqlens`` of length B+1); h0: (B,H,dk,dv) float32 or
-    None.  Returns (out, hT); out has q's dtype, hT is float32; rows of no
+    None.  A sequence's rows of a tensor, or a whole packed batch's, are
+    fewer than 2^31 bytes.  Returns (out, hT); out has q's dtype, hT is float32; rows of no
     sequence are not written.  Runs on the current stream (or ``stream``, with
     which the caller orders the tensors' other uses), asynchronously.
     ``workspace``: a uint8 device tensor of at least

@@ -45,10 +45,12 @@ extern "C" {
  *   shape, written; hT may be h0 itself (not a part of it).  A sequence of
  *   length 0 gets hT = h0 (or zeros).
  *
- * Sizes: B >= 0, T >= 0, H >= 1; dk, dv in {32, 64, 128}; fewer than 2^31
- *   bytes in a sequence's rows of one tensor (T * H * max(dk, dv) * element
- *   size; GDN_ERR_INVALID_ARG); H <= 65535, B * H < 2^18 and, dense, B * T <
- *   2^31.  dtype: GDN_F32 or GDN_BF16.
+ * Sizes: B >= 0, T >= 0, H >= 1; dk, dv in {32, 64, 128}; T * H * max(dk, dv)
+ *   * element size < 2^31 (GDN_ERR_INVALID_ARG): a sequence's rows are
+ *   addressed with 32 bits, and a packed batch, whose lengths the host does
+ *   not know, may hold one sequence of all T rows, so that there the bound is
+ *   the whole batch's (a larger one goes in several calls); H <= 65535, B * H <
+ *   2^18 and, dense, B * T < 2^31.  dtype: GDN_F32 or GDN_BF16.
  * Pointers: q, k, v and out are required when T > 0 and B > 0, g and hT when
  *   B > 0.  All are 16-byte aligned (GDN_ERR_INVALID_ARG otherwise; g and
  *   cu_seqlens 4-byte).  No output may overlap an input or another output,
