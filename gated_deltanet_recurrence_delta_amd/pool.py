@@ -167,10 +167,13 @@ class StatePool:
             raise ValueError("a slot is named twice")
         return slots
 
-    def _take(self, n):
+    def _take(self, n, src):
+        """n free slots with the state of slot ``src`` (-1: zeros), in use once their states are queued."""
         if not 0 <= n <= len(self._free):
             raise ValueError(f"{n} slots are wanted, {len(self._free)} are free")
-        got = [self._free.pop() for _ in range(n)]
+        got = self._free[len(self._free) - n:][::-1]
+        self._move([src] * n, got)
+        del self._free[len(self._free) - n:]
         self._live.update(got)
         return got
 
@@ -180,16 +183,12 @@ class StatePool:
 
     def alloc(self, n=1):
         """n slots with zero states."""
-        got = self._take(n)
-        self._move([-1] * n, got)
-        return got
+        return self._take(n, -1)
 
     def fork(self, slot, n=1):
         """n new slots that hold copies of ``slot``'s state."""
         self._check([slot])
-        got = self._take(n)
-        self._move([slot] * n, got)
-        return got
+        return self._take(n, slot)
 
     def copy(self, src, dst):
         """State of src[i] into dst[i], all at once; slots in use."""
