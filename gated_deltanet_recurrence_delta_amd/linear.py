@@ -103,6 +103,8 @@ def _raw_stream(dev, stream):
     import torch
 
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be one of {dev}, got one of {stream.device}")
         return stream.cuda_stream
     try:
         return torch._C._cuda_getCurrentRawStream(dev.index)  # without the Stream object around it
