@@ -77,3 +77,33 @@ def test_sequences_that_overlap(dtype, between):
     c["h0"] = torch.from_numpy(np.random.default_rng(2).standard_normal(got["hT"].shape).astype(np.float32)).cuda()
     got, at = run(c, cu)
     check(dict(hT=got["hT"], dh0=got["dh0"]), c, dtype, at)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 32)])
+def test_a_graph_takes_each_replays_offsets(dk, dv):
+    """Captured with one set of offsets, replayed with others: ascending, falling, with rows of no sequence."""
+    T, some = 1500, [[0, 700, 1500, 1500], [0, 0, 1, 1500], [600, 1500, 0, 600], [5, 400, 400, 1490], [1500, 0, 0, 900]]
+    c = make(dk + dv, "bf16", T, 2, dk, dv, 3, packed=True, slow=True)
+    assert gdn.gdn_linear_workspace_size(3, T, 2, dk, dv, 1, 1) > 0
+    cu = torch.tensor(some[0], dtype=torch.int32, device="cuda")
+
+    def call(cu):
+        out, hT = gdn.linear_fwd(c["q"], c["k"], c["v"], c["g"], c["h0"], cu)
+        return dict(out=out, hT=hT, **gdn.linear_bwd(c["q"], c["k"], c["v"], c["g"], c["dout"], c["h0"], cu, dhT=c["dhT"]))
+
+    call(cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(cu)
+    for at in some[1:] + some:
+        cu.copy_(torch.tensor(at, dtype=torch.int32))
+        graph.replay()
+        want = call(cu)
+        torch.cuda.synchronize()
+        inside = torch.zeros(T, dtype=torch.bool, device="cuda")
+        for b, e in zip(at, at[1:]):
+            inside[b:e] = True
+        for n in got:
+            x, y = (got[n], want[n]) if n in ("hT", "dh0") else (got[n][inside], want[n][inside])
+            assert torch.equal(x, y), (at, n)  # rows of no sequence hold what the graph's memory held
