@@ -30,11 +30,12 @@
 //
 // Bound by memory: every row is read once by one workgroup, or twice where
 // its chain is cut (two launches, see segment_chunks).  B=4 H=16 T=4096,
-// dx = dz = 128 bf16: 39 us for the segments' states, 61 us for the outputs,
-// 64 KB for each 64 rows of a workgroup in 3.2 us, 5.1 TB/s over the device (a
-// copy of the same size reaches 4.7); 11 us of each launch are its start, the
-// first chunks' way and the last stores.  512 chains uncut (2.1 GB): 479 us,
-// 4.5 TB/s.
+// dx = dz = 128 bf16 (medians): 41 us for the segments' states, 63 us for the
+// outputs, 64 KB for each 64 rows of a workgroup in 3.2 us, 5.1 TB/s over the
+// device (a copy of the same size reaches 4.7); 11 us of each launch are its
+// start, the first chunks' way and the last stores.  The outputs' launch reads
+// 218 MB from memory and writes 71, what its rows and states are.  512 chains
+// uncut (2.1 GB): 472 us, 4.5 TB/s.
 //
 // What was tried in its place, for the same call: workgroups of 32 state
 // columns, four to a chain, need no segments, but read x and y four times
@@ -85,7 +86,8 @@ struct LK {
   // 272 us where these take 260, 64,711 packed rows of 16 heads).  fp32: 16,
   // which leaves room for two workgroups on a CU (dx = 128, dz = 32, 512
   // chains of 4,096 rows: 594 us, with 32 rows 1,089), but 32 at 128 x 128,
-  // where there is room for one either way (700 us against 766).
+  // where there is room for one either way (256 chains of 4,096 rows: 713 us,
+  // with 16 rows 779).
   // The end states of segments, which need no scores, take twice the rows in
   // bf16: half the decays of the state (32,768 rows of 16 heads at 128 x 128:
   // 184 us, with 32 rows in both 199).

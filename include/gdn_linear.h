@@ -66,11 +66,13 @@ extern "C" {
  * returned; results are valid once the stream has been synchronised.  The
  * library allocates nothing and keeps no pointer.  Identical calls give
  * identical bits on one device (no atomics, fixed reduction order); how a
- * batch is cut into segments goes by B, T, H, dv alone, so the same sequence
- * in another batch may differ by rounding.
+ * batch is cut into segments goes by its sizes (B, T, H, dk, dv), the dtype,
+ * whether it is packed and the direction, so the same sequence in another
+ * batch may differ by rounding.
  *
  * Segments.  A long sequence of a batch with fewer chains than the device has
- * compute units is cut into segments that run side by side.  A first launch
+ * compute units is cut into segments that run side by side (a packed one
+ * where its offsets ascend).  A first launch
  * forms the state that each segment leaves, from which the next ones start;
  * rows whose decay to the segment's end is below e^-40 are left out of it (as
  * gdn_fwd's halos are bounded), non-finite ones among them.  With hT == h0
