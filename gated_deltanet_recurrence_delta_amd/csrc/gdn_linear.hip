@@ -180,7 +180,10 @@ constexpr double FORGOTTEN = 40.0;
 // registers: the compiler does not look into the assembly.)
 __device__ static inline void lds_copy(unsigned at, int off, __amdgpu_buffer_rsrc_t r) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(at), "v"(off), "s"(r) : "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(at), "v"(off), "s"(r)
+               : "m0");
 #endif
 }
 

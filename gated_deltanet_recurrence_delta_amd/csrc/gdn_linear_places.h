@@ -91,7 +91,8 @@ struct Places {
       } else {
         const int segs = (r.len + rows - 1) / rows;
         const int first = r.begin / rows + (PASS == 0 ? i : 0), count = PASS == 0 ? (segs > 1 ? segs : 1) : segs - 1;
-        if (at >= first && at < first + count) s.take(i, at - first);  // more than one only where an offset falls
+        // by several threads only where an offset falls; settle() overrules them there
+        if (at >= first && at < first + count) s.take(i, at - first);
       }
     }
   }
