@@ -20,7 +20,13 @@ __all__ = ["gdn_fwd", "gdn_fwd_train", "gdn_bwd_saved", "fwd_train", "gdn_fwd_sc
            "gdn_linear_fwd", "gdn_linear_fwd_recurrent", "gdn_linear_bwd", "gdn_linear_workspace_size", "linear_fwd",
            "linear_fwd_recurrent", "linear_bwd", "linear_attention", "gdn_fwd_recurrent_pool",
            "gdn_linear_fwd_recurrent_pool", "gdn_state_move", "fwd_recurrent_pool", "linear_fwd_recurrent_pool",
-           "state_move", "StatePool"]
+           "state_move", "StatePool",
+           # what stands around a recurrence: causal convolution, selective scan, norms with rotation
+           "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_workspace_size", "gdn_conv_fwd_pool", "conv_fwd", "conv_bwd",
+           "conv_fwd_pool", "causal_conv", "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_workspace_size",
+           "gdn_ssm_fwd_recurrent_pool", "ssm_fwd", "ssm_bwd", "ssm_fwd_recurrent_pool", "selective_scan",
+           "gdn_qk_norm_fwd", "gdn_qk_norm_bwd", "gdn_qk_norm_workspace_size", "qk_norm_fwd", "qk_norm_bwd",
+           "qk_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDN_LIB_PATH names another build of the same library (the tests use it to
@@ -98,6 +104,28 @@ def load():
         lib.gdn_linear_fwd_recurrent_pool.argtypes = [P] * 8 + [I] * 6 + [P, I]
         lib.gdn_state_move.restype = I
         lib.gdn_state_move.argtypes = [P, LL, LL, LL, P, P, I, P]
+        lib.gdn_conv_fwd.restype = I
+        lib.gdn_conv_fwd.argtypes = [P] * 7 + [I] * 4 + [P, I, I]
+        lib.gdn_conv_bwd.restype = I
+        lib.gdn_conv_bwd.argtypes = [P] * 11 + [I] * 4 + [P, I, I, P, LL]
+        lib.gdn_conv_workspace_size.restype = LL
+        lib.gdn_conv_workspace_size.argtypes = [I] * 6
+        lib.gdn_conv_fwd_pool.restype = I
+        lib.gdn_conv_fwd_pool.argtypes = [P] * 7 + [I] * 5 + [P, I, I]
+        lib.gdn_ssm_fwd.restype = I
+        lib.gdn_ssm_fwd.argtypes = [P] * 12 + [I] * 5 + [P, I, I, P, LL]
+        lib.gdn_ssm_bwd.restype = I
+        lib.gdn_ssm_bwd.argtypes = [P] * 21 + [I] * 5 + [P, I, I, P, LL]
+        lib.gdn_ssm_workspace_size.restype = LL
+        lib.gdn_ssm_workspace_size.argtypes = [I] * 8
+        lib.gdn_ssm_fwd_recurrent_pool.restype = I
+        lib.gdn_ssm_fwd_recurrent_pool.argtypes = [P] * 12 + [I] * 6 + [P, I, I]
+        lib.gdn_qk_norm_fwd.restype = I
+        lib.gdn_qk_norm_fwd.argtypes = [P] * 9 + [I] * 7 + [ctypes.c_float, P, I, I]
+        lib.gdn_qk_norm_bwd.restype = I
+        lib.gdn_qk_norm_bwd.argtypes = [P] * 13 + [I] * 7 + [ctypes.c_float, P, I, I, P, LL]
+        lib.gdn_qk_norm_workspace_size.restype = LL
+        lib.gdn_qk_norm_workspace_size.argtypes = [I] * 5
         lib.gdn_strerror.restype = ctypes.c_char_p
         lib.gdn_strerror.argtypes = [I]
         lib.gdn_version.restype = I
@@ -570,3 +598,9 @@ from .linear import (gdn_linear_bwd, gdn_linear_fwd, gdn_linear_fwd_recurrent,  
                      gdn_linear_workspace_size, linear_attention, linear_bwd, linear_fwd, linear_fwd_recurrent)
 from .pool import (StatePool, fwd_recurrent_pool, gdn_fwd_recurrent_pool,  # noqa: E402
                    gdn_linear_fwd_recurrent_pool, gdn_state_move, linear_fwd_recurrent_pool, state_move)
+from .conv import (causal_conv, conv_bwd, conv_fwd, conv_fwd_pool, gdn_conv_bwd, gdn_conv_fwd,  # noqa: E402
+                   gdn_conv_fwd_pool, gdn_conv_workspace_size)
+from .ssm import (gdn_ssm_bwd, gdn_ssm_fwd, gdn_ssm_fwd_recurrent_pool, gdn_ssm_workspace_size,  # noqa: E402
+                  selective_scan, ssm_bwd, ssm_fwd, ssm_fwd_recurrent_pool)
+from .qk_norm import (gdn_qk_norm_bwd, gdn_qk_norm_fwd, gdn_qk_norm_workspace_size, qk_norm, qk_norm_bwd,  # noqa: E402
+                      qk_norm_fwd)

@@ -9,7 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in ("gdn_fwd.hip", "gdn_fwd_full.hip", "gdn_recurrent.hip",
                                                 "gdn_diag.hip", "gdn_bwd.hip", "gdn_bwd_full.hip",
-                                                "gdn_linear.hip", "gdn_pool.hip")]
+                                                "gdn_linear.hip", "gdn_pool.hip", "gdn_conv.hip",
+                                                "gdn_ssm.hip", "gdn_qk_norm.hip")]
 LIB = os.path.join(HERE, "libgdn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

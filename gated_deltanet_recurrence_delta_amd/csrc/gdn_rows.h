@@ -1,0 +1,194 @@
+// Device-side building blocks of the operators around the recurrences: rows
+// read and written in vectors and computed in fp32, sums over neighbouring
+// lanes, and the segments of packed sequences.  Internal header: every
+// definition sits in an unnamed namespace of the including file.
+#ifndef GDN_ROWS_H
+#define GDN_ROWS_H
+
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+namespace {
+
+// ------------------------------------------------------------------ vectors --
+
+template <typename TI, int V>
+struct Raw {
+  typedef TI type __attribute__((ext_vector_type(V)));
+};
+template <typename TI>
+struct Raw<TI, 1> {
+  typedef TI type;
+};
+
+template <int V>
+struct Vals {
+  float v[V];
+  __device__ float& operator[](int i) { return v[i]; }
+  __device__ float operator[](int i) const { return v[i]; }
+};
+
+template <typename TI, int V>
+__device__ static inline typename Raw<TI, V>::type load_raw(const TI* p) {
+  return *reinterpret_cast<const typename Raw<TI, V>::type*>(p);
+}
+
+template <typename TI, int V>
+__device__ static inline Vals<V> widen(const typename Raw<TI, V>::type& r) {
+  Vals<V> x;
+  if constexpr (V == 1) x[0] = (float)r;
+  else
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = (float)r[i];
+  return x;
+}
+
+template <typename TI, int V>
+__device__ static inline Vals<V> load_vals(const TI* p) {
+  return widen<TI, V>(load_raw<TI, V>(p));
+}
+
+// Rounded to nearest even where TI is bf16.
+template <typename TI, int V>
+__device__ static inline void store_vals(TI* p, const Vals<V>& x) {
+  if constexpr (V == 1) {
+    *p = (TI)x[0];
+  } else {
+    typename Raw<TI, V>::type r;
+    if constexpr (sizeof(TI) == 2) {
+      // pair by pair: a packed conversion each
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+      typedef uint32_t u __attribute__((ext_vector_type(V / 2)));
+      u w;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{x[2 * i], x[2 * i + 1]}, b2));
+      r = __builtin_bit_cast(typename Raw<TI, V>::type, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) r[i] = x[i];
+    }
+    *reinterpret_cast<typename Raw<TI, V>::type*>(p) = r;
+  }
+}
+
+// --------------------------------------------------------------- functions --
+
+// 1 / (1 + exp(-x)); exp2 and the reciprocal are within 1 ulp, the product
+// with log2(e) moves the exponent by |x| 2^-24 at most.
+__device__ static inline float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// ------------------------------------------------------------- cross-lane --
+
+template <int CTRL>
+__device__ static inline float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over groups of L neighbouring lanes, in every lane of the group; the
+// same value, bit for bit, in each (sums of two are symmetric).
+template <int L>
+__device__ static inline float sum_lanes(float x) {
+  if constexpr (L >= 2) x += dpp<0xB1>(x);   // quad_perm 1 0 3 2
+  if constexpr (L >= 4) x += dpp<0x4E>(x);   // quad_perm 2 3 0 1
+  if constexpr (L >= 8) x += dpp<0x141>(x);  // mirror of 8 lanes: the other quad
+  if constexpr (L >= 16) x += dpp<0x140>(x); // mirror of 16 lanes: the other eight
+  if constexpr (L >= 32) x += __shfl_xor(x, 16);
+  if constexpr (L >= 64) x += __shfl_xor(x, 32);
+  return x;
+}
+
+// ---------------------------------------------------------------- segments --
+//
+// A launch works on segments of up to L rows, one a slot.  Dense sequences
+// have nseg slots each.  Of packed ones, sequence n has the slots from
+// begin(n) / L + n on: ceil(length / L) of them fit before the next one's, an
+// empty sequence has one, and the slots of all are fewer than T / L + B + 1.
+
+struct Segment {
+  long row0;   // the segment's first row
+  int n;       // sequence, -1: none
+  int t0;      // the first row's place in its sequence
+  int len;     // rows (0 for the one segment of an empty sequence)
+  int total;   // rows of the sequence
+  __device__ bool first() const { return t0 == 0; }
+  __device__ bool last() const { return t0 + len == total; }
+};
+
+// Rows of a call: places within a sequence and a few rows behind it are ints.
+constexpr long long MOST_ROWS = 1LL << 30;
+
+inline int segments_of(long long T, long long L) { return (int)(T > L ? (T + L - 1) / L : 1); }
+
+inline long long slots_of(bool packed, long long B, long long T, long long L) {
+  return packed ? T / L + B : B * segments_of(T, L);
+}
+
+__device__ static inline int taken(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// How many sequences begin at or before the slot: a search that looks at 64
+// offsets at once.  All 64 lanes take part, with one slot.
+__device__ static inline int sequences_before(const int32_t* cu, int B, int T, int L, long slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) >> 6;
+    const long at = lo + (long)lane * step;
+    const bool before = at < hi && taken(cu[at < hi ? at : lo], 0, T) / L + at <= slot;
+    const int c = __popcll(__ballot(before));
+    if (step == 1) return lo + c;
+    if (c == 0) return lo;
+    hi = (int)min((long)hi, lo + (long)c * step);
+    lo += (c - 1) * step + 1;
+  }
+  return lo;
+}
+
+__device__ static inline Segment segment_of(const int32_t* cu, int B, int T, int L, int nseg, long slot) {
+  Segment s;
+  int i;
+  if (cu) {
+    s.n = sequences_before(cu, B, T, L, slot) - 1;
+    if (s.n < 0) return Segment{0, -1, 0, 0, 0};
+    const int b = taken(cu[s.n], 0, T), e = taken(cu[s.n + 1], b, T);
+    s.total = e - b;
+    s.row0 = b;
+    i = (int)(slot - b / L - s.n);
+  } else {
+    s.n = (int)(slot / nseg);
+    s.total = T;
+    s.row0 = (long)s.n * T;
+    i = (int)(slot % nseg);
+  }
+  const long t0 = (long)i * L;
+  if (i < 0 || (i > 0 && t0 >= s.total)) return Segment{0, -1, 0, 0, 0};
+  s.t0 = (int)t0;
+  s.row0 += t0;
+  s.len = min(L, s.total - s.t0);
+  return s;
+}
+
+// A whole sequence as one segment; any offsets.
+__device__ static inline Segment sequence_of(const int32_t* cu, int T, int n) {
+  if (!cu) return Segment{(long)n * T, n, 0, T, T};
+  const int b = taken(cu[n], 0, T), e = taken(cu[n + 1], b, T);
+  return Segment{b, n, 0, e - b, e - b};
+}
+
+// The slot of sequence n in the pool, or -1: outside it, or an earlier
+// sequence's.  All 64 lanes take part, with one n.
+__device__ static inline int pool_slot(const int32_t* slots, int nslots, int n) {
+  const int slot = slots[n], lane = threadIdx.x & 63;
+  if ((unsigned)slot >= (unsigned)nslots) return -1;
+  for (int i = lane; i - lane < n; i += 64)
+    if (__ballot(i < n && slots[min(i, n)] == slot)) return -1;
+  return slot;
+}
+
+}  // namespace
+
+#endif  // GDN_ROWS_H

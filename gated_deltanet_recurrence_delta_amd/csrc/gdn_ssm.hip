@@ -1,0 +1,1070 @@
+// The selective state space scan, forwards, backwards and on states in a
+// pool, for gfx950.
+//
+// Per token, channel and state: a = exp(s A), h = a h + s x b, y += c h.  The
+// decay is each channel's, state's and token's own, so nothing of it is a
+// matrix product; what bounds the kernels is the vector unit: four
+// instructions and an exponential for each of B T D N state updates, against
+// some ten bytes of memory for each N of them.
+//
+// Forwards a lane owns a channel and holds its N states in registers; the
+// token's keys, the same for all channels of a group, come through the scalar
+// unit and cost no vector instruction.  Where channels and sequences are too
+// few to fill the device, sequences are cut into segments (gdn_ssm.h).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gdn_checks.h"
+#include "gdn_rows.h"
+#include "gdn_ssm.h"
+
+namespace {
+
+constexpr float LOG2E = 1.44269504f;
+
+struct SsmParams {
+  const void* x;
+  const void* dt;
+  const void* b;
+  const void* c;
+  const float* A_log;
+  const float* Dskip;
+  const void* z;
+  const float* dt_bias;
+  const float* h0;       // pooled: the pool
+  const int32_t* cu;
+  const int32_t* slots;  // null: sequence n has state n
+  void* out;
+  float* hT;
+  const void* dout;
+  const float* dhT;
+  void* dx;
+  void* ddt;
+  void* db;
+  void* dc;
+  float* dA_log;
+  float* dD;
+  void* dz;
+  float* ddt_bias;
+  float* dh0;
+  float* E;      // (segments, D, N): the state a segment leaves from zero; then the state it starts from
+  float* R;      // the same for the state's gradient, backwards in time
+  float* S;      // (segments, D): the sum of a segment's steps
+  float* keys;   // (tiles of workgroups, rows, G, 2, N): partial sums for db and dc
+  float* sums;   // (runs of segments, D, N + 2): partial sums for dA_log, dD and ddt_bias
+  int B, T, D, G, N, Dg, nslots;
+  int L, nseg;   // rows a segment, segments a dense sequence
+  long segments;
+  int run, runs; // backwards: segments a workgroup, and workgroups' runs
+  long rows;
+  int softplus;
+};
+
+// ------------------------------------------------------------------- steps --
+
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with q = e / (2
+// + e), log(1 + e) = 2 atanh(q): an odd polynomial of degree 9 in q <= 1/3,
+// fitted to 4e-9 relative.  Small steps keep their relative precision, which
+// log2(1 + e) would lose.
+__device__ static inline float softplus(float v) {
+  const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -LOG2E);
+  const float q = e * __builtin_amdgcn_rcpf(2.f + e), w = q * q;
+  float y = __builtin_fmaf(w, 0.281577796f, 0.279651582f);
+  y = __builtin_fmaf(w, y, 0.400245965f);
+  y = __builtin_fmaf(w, y, 0.666663229f);
+  y = __builtin_fmaf(w, y, 2.f);
+  return __builtin_fmaf(q, y, v > 0.f ? v : v - v);  // v - v: 0, and NaN for a NaN
+}
+
+__device__ static inline float step_of(float v, int soft) { return soft ? softplus(v) : v; }
+
+// -------------------------------------------------------------------- keys --
+
+// Sixteen values of a token's key through the scalar unit: the address is the
+// same in all lanes, and the constant address space says that nothing writes
+// there while the kernel runs.
+template <typename TI>
+struct Keys16 {
+  typedef uint32_t words __attribute__((ext_vector_type(sizeof(TI) * 4)));
+  words w;
+  __device__ void load(const TI* p) {
+    w = *(const __attribute__((address_space(4))) words*)(uintptr_t)p;
+  }
+  __device__ float operator[](int i) const {
+    // (a value first: a bit cast of a vector's element itself took element 0)
+    const uint32_t u = sizeof(TI) == 4 ? w[i] : i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16;
+    return __builtin_bit_cast(float, u);
+  }
+};
+
+// ---------------------------------------------------------- a lane a channel --
+
+// Tokens on their way at once.
+constexpr int FLIGHT = 4;
+
+// A wave's place: a segment, a group and 64 of its channels.
+struct Place {
+  Segment s;
+  long slot;
+  int g, d;
+  bool active;  // the lane's channel is one of the group's
+};
+
+// Waves of a workgroup take neighbouring tiles of 64 channels.
+__device__ static inline Place place_of(const SsmParams& p) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (p.Dg + 63) >> 6, quads = (tiles + 3) >> 2;
+  Place w;
+  int k = blockIdx.x;
+  const int tile = k % quads * 4 + wave;
+  k /= quads;
+  w.g = k % p.G;
+  w.slot = k / p.G;
+  if (tile >= tiles) {
+    w.s.n = -1;
+    return w;
+  }
+  w.s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, w.slot);
+  const int c = tile * 64 + lane;
+  w.active = c < p.Dg;
+  w.d = w.g * p.Dg + min(c, p.Dg - 1);
+  return w;
+}
+
+template <int N>
+__device__ static inline void load_states(Vals<N>& h, const float* p) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const Vals<4> q = load_vals<float, 4>(p + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[i + e] = q[e];
+  }
+}
+
+template <int N>
+__device__ static inline void store_states(float* p, const Vals<N>& h) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) store_vals<float, 4>(p + i, Vals<4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}});
+}
+
+// Forwards.  OUTPUT: the outputs from the segment's start state (E if the
+// sequences are cut, else h0).  Otherwise the state that a segment leaves from
+// zero, and the sum of its steps; what follows the last segment is hT, which
+// the outputs' launch gives.
+template <typename TI, int N, bool OUTPUT>
+__global__ __launch_bounds__(256) void ssm_kernel(const SsmParams p) {
+  const Place w = place_of(p);
+  if (w.s.n < 0 || (!OUTPUT && w.s.last())) return;
+  const int D = p.D, d = w.d;
+  const long KS = (long)p.G * N;
+  Vals<N> A, h;
+  load_states<N>(A, p.A_log + (long)d * N);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    A[i] = -LOG2E * expf(A[i]);
+    h[i] = 0.f;
+  }
+  if constexpr (OUTPUT) {
+    if (p.E) load_states<N>(h, p.E + (w.slot * D + d) * N);
+    else if (p.h0) load_states<N>(h, p.h0 + ((long)w.s.n * D + d) * N);
+  }
+  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = OUTPUT && p.Dskip ? p.Dskip[d] : 0.f;
+  const long at = w.s.row0 * D + d;
+  const TI* x = static_cast<const TI*>(p.x) + at;
+  const TI* dt = static_cast<const TI*>(p.dt) + at;
+  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
+  TI* out = static_cast<TI*>(p.out) + at;
+  const TI* bk = static_cast<const TI*>(p.b) + (w.s.row0 * p.G + w.g) * N;
+  const TI* ck = static_cast<const TI*>(p.c) + (w.s.row0 * p.G + w.g) * N;
+  const int len = w.s.len;
+  float S = 0.f;
+
+  TI xn[FLIGHT], dn[FLIGHT], zn[FLIGHT];
+#pragma unroll
+  for (int f = 0; f < FLIGHT; ++f) {
+    const long o = (long)min(f, max(len - 1, 0)) * D;
+    if (len > 0) {
+      xn[f] = x[o];
+      dn[f] = dt[o];
+      if (OUTPUT) zn[f] = z[o];
+    }
+  }
+  Keys16<TI> bn, cn;
+  if (len > 0) {
+    bn.load(bk);
+    if (OUTPUT) cn.load(ck);
+  }
+  for (int t = 0; t < len; t += FLIGHT) {
+    TI xr[FLIGHT], dr[FLIGHT], zr[FLIGHT];
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) {
+      xr[f] = xn[f];
+      dr[f] = dn[f];
+      if (OUTPUT) zr[f] = zn[f];
+      const long o = (long)min(t + FLIGHT + f, len - 1) * D;
+      xn[f] = x[o];
+      dn[f] = dt[o];
+      if (OUTPUT) zn[f] = z[o];
+    }
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) {
+      if (t + f >= len) break;
+      const float xv = (float)xr[f], s = step_of((float)dr[f] + bias, p.softplus), u = s * xv;
+      float y = 0.f;
+      if constexpr (!OUTPUT) S += s;
+#pragma unroll
+      for (int n = 0; n < N; n += 16) {
+        const Keys16<TI> bv = bn, cv = cn;
+        // the next sixteen
+        const long next = n + 16 < N ? (long)(t + f) * KS + n + 16 : (long)min(t + f + 1, len - 1) * KS;
+        bn.load(bk + next);
+        if (OUTPUT) cn.load(ck + next);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = __builtin_amdgcn_exp2f(s * A[n + i]);
+          h[n + i] = __builtin_fmaf(a, h[n + i], u * bv[i]);
+          if constexpr (OUTPUT) y = __builtin_fmaf(cv[i], h[n + i], y);
+        }
+      }
+      if constexpr (OUTPUT) {
+        y = __builtin_fmaf(skip, xv, y);
+        if (p.z) {
+          const float zv = (float)zr[f];
+          y *= zv * sigmoid(zv);
+        }
+        if (w.active) out[(long)(t + f) * D] = (TI)y;
+      }
+    }
+  }
+  if (!w.active) return;
+  if constexpr (OUTPUT) {
+    if (w.s.last()) store_states<N>(p.hT + ((long)w.s.n * D + d) * N, h);
+  } else {
+    store_states<N>(p.E + (w.slot * D + d) * N, h);
+    p.S[w.slot * D + d] = S;
+  }
+}
+
+// Joins the segments of each sequence: a thread is one state.  Forwards E, the
+// state each segment leaves from zero, becomes the one it starts from;
+// backwards in time R, likewise, for the state's gradient (blockIdx.y == 1).
+__device__ static inline void join_state(const SsmParams& p, long DN, long id, bool back) {
+  const int n = (int)(id / DN);
+  const long r = id - n * DN;
+  const int d = (int)(r / p.N);
+  long slot = (long)n * p.nseg;
+  int count = p.nseg;
+  if (p.cu) {
+    const int b = taken(p.cu[n], 0, p.T), e = taken(p.cu[n + 1], b, p.T);
+    slot = b / p.L + n;
+    count = (int)min((long)(e - b + p.L - 1) / p.L, max(p.segments - slot, 0L));
+  } else if (p.T == 0) {
+    count = 0;
+  }
+  const float A = -LOG2E * expf(p.A_log[r]);
+  float* state = (back ? p.R : p.E) + r;
+  const float* first = back ? p.dhT : p.h0;
+  float h = first ? first[id] : 0.f;
+  constexpr int F = 8;  // segments on their way at once
+  for (int i = 0; i < count; i += F) {
+    float e[F], s[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const long k = slot + (back ? count - 1 - min(i + f, count - 1) : min(i + f, count - 1));
+      e[f] = state[k * DN];
+      s[f] = p.S[k * p.D + d];
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+      if (i + f < count) {
+        const long k = slot + (back ? count - 1 - (i + f) : i + f);
+        state[k * DN] = h;
+        // the last segment's own state is not needed forwards, nor formed where outputs are
+        h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * s[f]), h, e[f]);
+      }
+  }
+  if (back) {
+    if (p.dh0) p.dh0[id] = h;
+  } else if (count == 0) {
+    p.E[((long)(p.cu ? taken(p.cu[n], 0, p.T) / p.L + n : slot)) * DN + r] = h;  // an empty sequence's one segment
+  }
+}
+
+__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
+  const long DN = (long)p.D * p.N;
+  for (long id = (long)blockIdx.x * 256 + threadIdx.x; id < p.B * DN; id += (long)gridDim.x * 256)
+    join_state(p, DN, id, blockIdx.y);
+}
+
+// --------------------------------------------------------- token by token --
+
+// Few tokens on states read and written once: a lane holds four neighbouring
+// states (16 bytes), so that a wave's accesses cover whole lines; N / 4 lanes
+// are a channel.
+template <typename TI, int N>
+__global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
+  constexpr int LC = N / 4, CH = 256 / LC;
+  const int tiles = (p.D + CH - 1) / CH;
+  const int n = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+  const int lane = threadIdx.x % LC, d0 = tile * CH + threadIdx.x / LC;
+  const Segment s = sequence_of(p.cu, p.T, n);
+  int state = n;
+  if (p.slots) state = pool_slot(p.slots, p.nslots, n);
+  if (d0 >= p.D) return;
+  const int D = p.D, d = d0;
+  const long at = s.row0 * D + d;
+  TI* out = static_cast<TI*>(p.out) + at;
+  if (state < 0) {
+    if (lane == 0)
+      for (int t = 0; t < s.len; ++t) out[(long)t * D] = (TI)0.f;
+    return;
+  }
+  const long sat = ((long)state * D + d) * N + lane * 4;
+  Vals<4> h = {{0.f, 0.f, 0.f, 0.f}}, A = load_vals<float, 4>(p.A_log + (long)d * N + lane * 4);
+  if (p.h0) h = load_vals<float, 4>(p.h0 + sat);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = -LOG2E * expf(A[i]);
+  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.Dskip ? p.Dskip[d] : 0.f;
+  const TI* x = static_cast<const TI*>(p.x) + at;
+  const TI* dt = static_cast<const TI*>(p.dt) + at;
+  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
+  const long key = (s.row0 * p.G + d / p.Dg) * N + lane * 4, KS = (long)p.G * N;
+  const TI* bk = static_cast<const TI*>(p.b) + key;
+  const TI* ck = static_cast<const TI*>(p.c) + key;
+  TI xn = {}, dn = {}, zn = {};
+  typename Raw<TI, 4>::type bn = {}, cn = {};
+  if (s.len > 0) {
+    xn = x[0];
+    dn = dt[0];
+    zn = z[0];
+    bn = load_raw<TI, 4>(bk);
+    cn = load_raw<TI, 4>(ck);
+  }
+  for (int t = 0; t < s.len; ++t) {
+    const float xv = (float)xn, v = (float)dn + bias, zv = (float)zn;
+    const Vals<4> b = widen<TI, 4>(bn), c = widen<TI, 4>(cn);
+    const int f = min(t + 1, s.len - 1);
+    xn = x[(long)f * D];
+    dn = dt[(long)f * D];
+    zn = z[(long)f * D];
+    bn = load_raw<TI, 4>(bk + f * KS);
+    cn = load_raw<TI, 4>(ck + f * KS);
+    const float st = step_of(v, p.softplus), u = st * xv;
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(st * A[i]), h[i], u * b[i]);
+      y = __builtin_fmaf(c[i], h[i], y);
+    }
+    y = __builtin_fmaf(skip, xv, sum_lanes<LC>(y));
+    if (p.z) y *= zv * sigmoid(zv);
+    if (lane == 0) out[(long)t * D] = (TI)y;
+  }
+  store_vals<float, 4>(p.hT + sat, h);
+}
+
+// ---------------------------------------------------------------- backwards --
+//
+// Segments of BL tokens.  A first launch forms, for sixteen states of a
+// channel, what a segment leaves from zero: the state E going forwards and,
+// going backwards in time, the state's gradient, R = sum_t exp(A (s_1 + .. +
+// s_t)) c_t dy_t, which one forward walk gives too.  The join makes of them the
+// state a segment starts from and the gradient that reaches its end.
+
+template <typename TI>
+__device__ static inline void bwd_map(const SsmParams& p, long k, int tiles, int parts) {
+  const int lane = threadIdx.x & 63, part = (int)(k % parts);
+  k /= parts;
+  const int tile = (int)(k % tiles);
+  k /= tiles;
+  const int g = (int)(k % p.G);
+  const long slot = k / p.G;
+  const Segment s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, slot);
+  if (s.n < 0) return;
+  const int c = tile * 64 + lane, D = p.D, d = g * p.Dg + min(c, p.Dg - 1), N = p.N;
+  const long KS = (long)p.G * N, sat = (slot * D + d) * N + part * 16;
+  Vals<16> A, E, P, R;
+  load_states<16>(A, p.A_log + (long)d * N + part * 16);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    A[i] = -LOG2E * expf(A[i]);
+    E[i] = R[i] = 0.f;
+    P[i] = 1.f;
+  }
+  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
+  const long at = s.row0 * D + d;
+  const TI* x = static_cast<const TI*>(p.x) + at;
+  const TI* dt = static_cast<const TI*>(p.dt) + at;
+  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
+  const TI* dout = static_cast<const TI*>(p.dout) + at;
+  const TI* bk = static_cast<const TI*>(p.b) + (s.row0 * p.G + g) * N + part * 16;
+  const TI* ck = static_cast<const TI*>(p.c) + (s.row0 * p.G + g) * N + part * 16;
+  const int len = s.len;
+  float S = 0.f;
+  TI xn[FLIGHT], dn[FLIGHT], zn[FLIGHT], gn[FLIGHT];
+  Keys16<TI> bn, cn;
+  if (len > 0) {
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) {
+      const long o = (long)min(f, len - 1) * D;
+      xn[f] = x[o];
+      dn[f] = dt[o];
+      zn[f] = z[o];
+      gn[f] = dout[o];
+    }
+    bn.load(bk);
+    cn.load(ck);
+  }
+  for (int t = 0; t < len; t += FLIGHT) {
+    TI xr[FLIGHT], dr[FLIGHT], zr[FLIGHT], gr[FLIGHT];
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) {
+      xr[f] = xn[f];
+      dr[f] = dn[f];
+      zr[f] = zn[f];
+      gr[f] = gn[f];
+      const long o = (long)min(t + FLIGHT + f, len - 1) * D;
+      xn[f] = x[o];
+      dn[f] = dt[o];
+      zn[f] = z[o];
+      gn[f] = dout[o];
+    }
+#pragma unroll
+    for (int f = 0; f < FLIGHT; ++f) {
+      if (t + f >= len) break;
+      const float st = step_of((float)dr[f] + bias, p.softplus), u = st * (float)xr[f];
+      float dy = (float)gr[f];
+      if (p.z) {
+        const float zv = (float)zr[f];
+        dy *= zv * sigmoid(zv);
+      }
+      S += st;
+      const Keys16<TI> bv = bn, cv = cn;
+      const long next = (long)min(t + f + 1, len - 1) * KS;
+      bn.load(bk + next);
+      cn.load(ck + next);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float a = __builtin_amdgcn_exp2f(st * A[i]);
+        E[i] = __builtin_fmaf(a, E[i], u * bv[i]);
+        P[i] *= a;
+        R[i] = __builtin_fmaf(P[i], dy * cv[i], R[i]);
+      }
+    }
+  }
+  if (c >= p.Dg) return;
+  store_states<16>(p.E + sat, E);
+  store_states<16>(p.R + sat, R);
+  if (part == 0) p.S[slot * D + d] = S;
+}
+
+template <typename TI>
+__global__ __launch_bounds__(256) void ssm_bwd_maps_kernel(const SsmParams p) {
+  // units: (segment, group, tile of 64 channels, sixteen of the states)
+  const int tiles = (p.Dg + 63) >> 6, parts = p.N / 16;
+  const long units = p.segments * p.G * tiles * parts;
+  for (long k = (long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < units;
+       k += (long)gridDim.x * 4)
+    bwd_map<TI>(p, k, tiles, parts);
+}
+
+// The gradients.  A wave has 1024 / N channels and all their states; a lane has
+// a block of four channels (its group's) by four states (its slice's), so that
+// half of both sums, over states and over channels, is within the lane.  Lane
+// 4 i + j also owns channel j of its group for what is the channel's alone: the
+// step, the gate, the stores.  Those values go to the other lanes by DPP.
+//
+// A segment is NB blocks of BT tokens.  A walk forwards keeps the states at the
+// blocks' starts; then, from the last block on, a block's states are formed
+// again and kept in registers, and its tokens are taken backwards.
+
+constexpr int BT = 8, NB = 4, BL = BT * NB;
+
+template <int J>
+__device__ static inline float from_quad(float x) {
+  return dpp<J * 0x55>(x);
+}
+
+__device__ static inline Vals<4> quad(float x) {
+  return {{from_quad<0>(x), from_quad<1>(x), from_quad<2>(x), from_quad<3>(x)}};
+}
+
+// Four sums over a quad's lanes, one for each of its channels: lane j gets the
+// j-th, and with more than four lanes a channel, the sum over all of them.
+template <int LC>
+__device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
+  const float a = (odd ? v[1] : v[0]) + dpp<0xB1>(odd ? v[0] : v[1]);
+  const float b = (odd ? v[3] : v[2]) + dpp<0xB1>(odd ? v[2] : v[3]);
+  float r = (high ? b : a) + dpp<0x4E>(high ? a : b);
+  if constexpr (LC == 8) r += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(r), (4 << 10) | 0x1f));
+  if constexpr (LC == 16) {
+    r += dpp<0x128>(r);  // row_ror 8
+    r += dpp<0x124>(r);  // row_ror 4
+  }
+  return r;
+}
+
+// a and b become (a's lanes below 32, b's below 32) and (a's from 32 on, b's
+// from 32 on): their sum then holds a's over both halves in the lower lanes
+// and b's in the upper ones, one instruction and one addition for two sums.
+// swap_rows does the same within each half, sixteen lanes by sixteen.
+__device__ static inline void swap_halves(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ static inline void swap_rows(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+
+template <typename TI, int N>
+__global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
+  constexpr int LC = N / 4;            // lanes a channel
+  constexpr int CT = 1024 / N;         // channels a wave
+  __shared__ __attribute__((aligned(16))) float key[BL][2][N];
+  __shared__ __attribute__((aligned(16))) float start[4][NB - 2][16][64];
+  __shared__ float steps[4][BL][64];
+  __shared__ __attribute__((aligned(16))) float part[2][4][BT][2][N];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = (p.Dg + CT - 1) / CT, quads = (tiles + 3) >> 2;
+  int k = blockIdx.x;
+  const int tq = k % quads;
+  k /= quads;
+  const int g = k % p.G, run = k / p.G;
+  const int D = p.D, tile = tq * 4 + wave;
+  const int slice = lane % LC, group = lane / LC;
+  const bool odd = lane & 1, high = lane & 2;
+  // channels of the lane's block, and its own
+  const int c0 = tile * CT + group * 4, cown = c0 + (lane & 3);
+  // Lanes behind the group's last channel work on copies of it, with inputs and
+  // gradients of zero, so that they add nothing to the sums over channels.
+  const bool real = cown < p.Dg, mine = real && slice < 4;
+  const int own = g * p.Dg + min(cown, p.Dg - 1);
+  int ch[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) ch[c] = g * p.Dg + min(c0 + c, p.Dg - 1);
+
+  float A[4][4], dA[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const Vals<4> a = load_vals<float, 4>(p.A_log + (long)ch[c] * N + slice * 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      A[c][j] = -LOG2E * expf(a[j]);
+      dA[c][j] = 0.f;
+    }
+  }
+  const float bias = p.dt_bias ? p.dt_bias[own] : 0.f, skip = p.Dskip ? p.Dskip[own] : 0.f;
+  float dD = 0.f, dbias = 0.f;
+  const TI* xs = static_cast<const TI*>(p.x);
+  const TI* dts = static_cast<const TI*>(p.dt);
+  const TI* zs = static_cast<const TI*>(p.z);
+  const TI* gs = static_cast<const TI*>(p.dout);
+  const TI* bs = static_cast<const TI*>(p.b);
+  const TI* cs = static_cast<const TI*>(p.c);
+  int turn = 0;
+
+  for (int r = 0; r < p.run; ++r) {
+    const long slot = (long)run * p.run + r;
+    if (slot >= p.segments) break;
+    const Segment s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, slot);
+    if (s.n < 0 || s.len == 0) continue;
+    const long row0 = s.row0;
+    const int len = s.len;
+    __syncthreads();  // the keys of the segment before have been read
+    for (int i = tid; i < len * N; i += 256) {
+      const int t = i / N, n = i % N;
+      const long o = ((row0 + t) * p.G + g) * N + n;
+      key[t][0][n] = (float)bs[o];
+      key[t][1][n] = (float)cs[o];
+    }
+    __syncthreads();
+
+    float h[4][4], l[4][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const long o = (slot * D + ch[c]) * N + slice * 4;
+      const Vals<4> e = load_vals<float, 4>(p.E + o), q = load_vals<float, 4>(p.R + o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[c][j] = e[j];
+        l[c][j] = q[j];  // exp(s A) times the next token's gradient
+      }
+    }
+    const int blocks = (len + BT - 1) / BT;
+    // steps of all tokens; the states at the blocks' starts
+#pragma unroll 1
+    for (int t = 0; t < blocks * BT; ++t) {
+      const long o = (row0 + min(t, len - 1)) * D + own;
+      const float st = t < len ? step_of((float)dts[o] + bias, p.softplus) : 0.f;
+      steps[wave][t][lane] = st;
+      if (t >= (blocks - 1) * BT) continue;
+      const Vals<4> sv = quad(st), uv = quad(st * (float)xs[o]);
+      const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[c][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[c] * A[c][j]), h[c][j], uv[c] * b[j]);
+      if ((t + 1) % BT == 0 && t + 1 < (blocks - 1) * BT) {
+        const int m = (t + 1) / BT - 1;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) start[wave][m][e][lane] = h[e >> 2][e & 3];
+      }
+    }
+
+#pragma unroll 1
+    for (int blk = blocks - 1; blk >= 0; --blk) {
+      const int t0 = blk * BT, cnt = min(BT, len - t0);
+      if (blk < blocks - 1) {
+        if (blk > 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) h[e >> 2][e & 3] = start[wave][blk - 1][e][lane];
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const Vals<4> e = load_vals<float, 4>(p.E + (slot * D + ch[c]) * N + slice * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[c][j] = e[j];
+          }
+        }
+      }
+      // forwards: the states before each token; outputs for the gate's gradient
+      float before[BT][4][4], xo[BT], dyo[BT];
+#pragma unroll
+      for (int i = 0; i < BT; ++i) {
+        const int t = t0 + i;
+        const bool there = i < cnt;
+        const long o = (row0 + min(t, len - 1)) * D + own;
+        const float x = there && real ? (float)xs[o] : 0.f;
+        float dy = there && real ? (float)gs[o] : 0.f;
+        const float st = steps[wave][t][lane];
+        xo[i] = x;
+        const Vals<4> sv = quad(st), uv = quad(st * x);
+        const Vals<4> b = load_vals<float, 4>(&key[min(t, len - 1)][0][slice * 4]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            before[i][c][j] = h[c][j];
+            h[c][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[c] * A[c][j]), h[c][j], uv[c] * b[j]);
+          }
+        if (p.z) {
+          const float z = (float)zs[o], q = sigmoid(z);
+          if (p.dz) {
+            const Vals<4> c4 = load_vals<float, 4>(&key[min(t, len - 1)][1][slice * 4]);
+            Vals<4> y;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              y[c] = 0.f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[c] = __builtin_fmaf(c4[j], h[c][j], y[c]);
+            }
+            const float yo = __builtin_fmaf(skip, x, sum_own<LC>(y, odd, high));
+            if (mine && there)
+              static_cast<TI*>(p.dz)[o] = (TI)(dy * yo * (q * __builtin_fmaf(z, 1.f - q, 1.f)));
+          }
+          dy *= z * q;
+        }
+        dyo[i] = dy;
+      }
+      // backwards
+#pragma unroll
+      for (int i = BT - 1; i >= 0; --i) {
+        const int t = t0 + i;
+        if (i < cnt) {
+          const float st = steps[wave][t][lane];
+          const Vals<4> sv = quad(st), uv = quad(st * xo[i]), gv = quad(dyo[i]);
+          const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]), cc = load_vals<float, 4>(&key[t][1][slice * 4]);
+          Vals<4> lb, mA, db, dc;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) lb[c] = mA[c] = db[c] = dc[c] = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float now = i == BT - 1 ? h[c][j] : before[i + 1 < BT ? i + 1 : i][c][j];
+              const float lv = __builtin_fmaf(cc[j], gv[c], l[c][j]);
+              db[j] = __builtin_fmaf(lv, uv[c], db[j]);
+              lb[c] = __builtin_fmaf(lv, b[j], lb[c]);
+              dc[j] = __builtin_fmaf(now, gv[c], dc[j]);
+              l[c][j] = lv * __builtin_amdgcn_exp2f(sv[c] * A[c][j]);
+              const float m = l[c][j] * before[i][c][j];
+              mA[c] = __builtin_fmaf(m, A[c][j], mA[c]);
+              dA[c][j] = __builtin_fmaf(m, sv[c], dA[c][j]);
+            }
+          const float lbo = sum_own<LC>(lb, odd, high), mAo = sum_own<LC>(mA, odd, high);
+          const long o = (row0 + t) * D + own;
+          // A is held times log2(e)
+          float ds = __builtin_fmaf(xo[i], lbo, mAo * 0.693147181f);
+          if (p.softplus) ds *= sigmoid((float)dts[o] + bias);
+          const float dx = __builtin_fmaf(st, lbo, skip * dyo[i]);
+          if (mine) {
+            static_cast<TI*>(p.dx)[o] = (TI)dx;
+            static_cast<TI*>(p.ddt)[o] = (TI)ds;
+            dD = __builtin_fmaf(dyo[i], xo[i], dD);
+            dbias += ds;
+          }
+          // the sums over the channels' lanes, LC apart
+          swap_halves(db[0], db[2]);
+          swap_halves(db[1], db[3]);
+          swap_halves(dc[0], dc[2]);
+          swap_halves(dc[1], dc[3]);
+          float d0 = db[0] + db[2], d1 = db[1] + db[3], e0 = dc[0] + dc[2], e1 = dc[1] + dc[3];
+          swap_rows(d0, d1);
+          swap_rows(e0, e1);
+          float sd = d0 + d1, se = e0 + e1;
+          // lanes 0..15 hold state 0 of the slice, 16..31 state 1, 32..47 state 2, 48..63 state 3
+          if constexpr (LC <= 8) {
+            sd += dpp<0x128>(sd);
+            se += dpp<0x128>(se);
+          }
+          if constexpr (LC == 4) {
+            sd += dpp<0x124>(sd);
+            se += dpp<0x124>(se);
+          }
+          if ((lane & 15) < LC) {
+            const int n = slice * 4 + (lane >> 4);
+            part[turn][wave][i][0][n] = sd;
+            part[turn][wave][i][1][n] = se;
+          }
+        }
+      }
+      __syncthreads();
+      for (int e = tid; e < cnt * 2 * N; e += 256) {
+        const float* q = &part[turn][0][0][0][0] + e;
+        constexpr int W = BT * 2 * N;
+        const float v = (q[0] + q[W]) + (q[2 * W] + q[3 * W]);
+        const int i = e / (2 * N), which = e / N % 2, n = e % N;
+        const long o = ((row0 + t0 + i) * p.G + g) * N + n;
+        if (quads == 1) static_cast<TI*>(which ? p.dc : p.db)[o] = (TI)v;
+        else p.keys[(((long)tq * p.rows + row0 + t0 + i) * p.G + g) * 2 * N + which * N + n] = v;
+      }
+      turn ^= 1;
+    }
+  }
+
+  float* sums = p.sums + (long)run * D * (N + 2);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c0 + c < p.Dg)
+      store_vals<float, 4>(sums + (long)ch[c] * N + slice * 4, Vals<4>{{dA[c][0], dA[c][1], dA[c][2], dA[c][3]}});
+  if (mine) {
+    sums[(long)D * N + own] = dD;
+    sums[(long)D * (N + 1) + own] = dbias;
+  }
+}
+
+// db and dc of the workgroups' sums, where a group's channels are several
+// workgroups'.  Rows of no sequence are left as they were.
+template <typename TI>
+__global__ __launch_bounds__(256) void ssm_keys_kernel(const SsmParams p, int quads) {
+  const long GN = (long)p.G * p.N, total = p.rows * GN * 2;
+  for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long)gridDim.x * 256) {
+    const int n = (int)(e % p.N), which = (int)(e / p.N % 2);
+    const long rg = e / (2 * p.N), row = rg / p.G;
+    if (p.cu && (row < p.cu[0] || row >= p.cu[p.B])) continue;
+    float a = 0.f;
+    for (int q = 0; q < quads; ++q) a += p.keys[(long)q * total + e];
+    static_cast<TI*>(which ? p.dc : p.db)[rg * p.N + n] = (TI)a;
+  }
+}
+
+// The parameters' gradients: 64 of them a workgroup, 16 threads each.
+__global__ __launch_bounds__(1024) void ssm_sums_kernel(const SsmParams p) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, k = threadIdx.x >> 6;
+  const long DN = (long)p.D * p.N, cols = DN + 2L * p.D, c = (long)blockIdx.x * 64 + lane;
+  float a = 0.f;
+  if (c < cols)
+#pragma unroll 4
+    for (int i = k; i < p.runs; i += 16) a += p.sums[i * cols + c];
+  sums[k][lane] = a;
+  __syncthreads();
+  if (k == 0 && c < cols) {
+    for (int i = 1; i < 16; ++i) a += sums[i][lane];
+    if (c < DN) p.dA_log[c] = -expf(p.A_log[c]) * a;
+    else if (c < DN + p.D) {
+      if (p.dD) p.dD[c - DN] = a;
+    } else if (p.ddt_bias) {
+      p.ddt_bias[c - DN - p.D] = a;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+inline long long up16(long long x) { return (x + 15) & ~15LL; }
+
+int tiles_of(int Dg, int channels) { return (Dg + channels - 1) / channels; }
+
+int sizes_checked(int B, int T, int D, int G, int N, bool packed, int dtype) {
+  if (B < 0 || T < 0 || D < 1 || G < 1 || N < 1 || D % G || (dtype != GDN_F32 && dtype != GDN_BF16))
+    return GDN_ERR_INVALID_ARG;
+  if ((packed ? 1LL : (long long)B) * T > MOST_ROWS || D >= 1 << 20 || B >= 1 << 24 || (long long)B * D >= 1 << 28)
+    return GDN_ERR_INVALID_ARG;
+  if (N != 16 && N != 32 && N != 64) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+// How a forward call runs.
+struct Cut {
+  bool recurrent;  // token by token, lanes across the states
+  int L, nseg;
+  long long segments;
+  bool cut() const { return segments > 0; }
+};
+
+// Waves that keep the device busy: four on each of its 1,024 vector units.
+constexpr long long WAVES = 4096;
+
+Cut cut_of(int B, int T, int D, int G, bool packed) {
+  Cut c = {false, std::max(T, 1), 1, 0};
+  if (B == 0) return c;
+  const long long tiles = (long long)G * tiles_of(D / G, 64), chains = B * tiles;
+  if (T <= 64) {
+    c.recurrent = true;
+    return c;
+  }
+  if (!packed && chains >= WAVES / 2) return c;
+  const long long rows = packed ? T : (long long)B * T;
+  const long long L = (rows * tiles + WAVES - 1) / WAVES;
+  c.L = (int)std::max(32LL, (L + 15) / 16 * 16);
+  if (c.L >= T) {
+    c.L = T;
+    return c;
+  }
+  c.nseg = segments_of(T, c.L);
+  c.segments = slots_of(packed, B, T, c.L);
+  return c;
+}
+
+// The pieces of a workspace.
+struct Space {
+  long long E, R, S, keys, sums, bytes;
+};
+
+Space space_of(long long segments, long long runs, long long rows, int D, int G, int N, int quads, bool back) {
+  Space w = {};
+  const long long state = up16(segments * D * N * 4);
+  w.E = 0;
+  w.R = w.E + state;
+  w.S = w.R + (back ? state : 0);
+  w.keys = w.S + up16(segments * D * 4);
+  w.sums = w.keys + (back && quads > 1 ? up16(rows * G * 2 * N * 4 * quads) : 0);
+  w.bytes = w.sums + (back ? up16(runs * D * (N + 2) * 4) : 0);
+  return w;
+}
+
+struct BackPlan {
+  long long segments, runs, rows;
+  int nseg, run, quads;
+};
+
+BackPlan back_plan(int B, int T, int D, int G, int N, bool packed) {
+  BackPlan b;
+  b.rows = (packed ? 1LL : B) * (long long)T;
+  b.nseg = segments_of(T, BL);
+  b.segments = B > 0 ? slots_of(packed, B, T, BL) : 0;
+  b.quads = tiles_of(tiles_of(D / G, 1024 / N), 4);
+  // Workgroups in two rounds or more on 512 places (two a compute unit), each
+  // with as many segments as that leaves: few partial sums.
+  const long long wide = (long long)b.quads * G;
+  b.run = (int)std::max(1LL, b.segments * wide / 1024);
+  b.runs = (b.segments + b.run - 1) / b.run;
+  return b;
+}
+
+template <typename TI>
+void launch_outputs(const SsmParams& p, unsigned grid, bool output, hipStream_t s) {
+  const dim3 g(grid), b(256);
+  switch (p.N) {
+    case 16:
+      if (output) hipLaunchKernelGGL((ssm_kernel<TI, 16, true>), g, b, 0, s, p);
+      else hipLaunchKernelGGL((ssm_kernel<TI, 16, false>), g, b, 0, s, p);
+      break;
+    case 32:
+      if (output) hipLaunchKernelGGL((ssm_kernel<TI, 32, true>), g, b, 0, s, p);
+      else hipLaunchKernelGGL((ssm_kernel<TI, 32, false>), g, b, 0, s, p);
+      break;
+    default:
+      if (output) hipLaunchKernelGGL((ssm_kernel<TI, 64, true>), g, b, 0, s, p);
+      else hipLaunchKernelGGL((ssm_kernel<TI, 64, false>), g, b, 0, s, p);
+  }
+}
+
+template <typename TI>
+void launch_recurrent(const SsmParams& p, unsigned grid, hipStream_t s) {
+  const dim3 g(grid), b(256);
+  if (p.N == 16) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 16>), g, b, 0, s, p);
+  else if (p.N == 32) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 32>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 64>), g, b, 0, s, p);
+}
+
+template <typename TI>
+void launch_bwd(const SsmParams& p, unsigned grid, hipStream_t s) {
+  const dim3 g(grid), b(256);
+  if (p.N == 16) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 16>), g, b, 0, s, p);
+  else if (p.N == 32) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 32>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((ssm_bwd_kernel<TI, 64>), g, b, 0, s, p);
+}
+
+constexpr long long MOST_WGS = (1LL << 24) - 1;  // a grid holds fewer than 2^32 threads; the launches that may need more loop
+
+int forward(SsmParams p, int dtype, int flags, void* workspace, long long workspace_bytes, void* stream) {
+  const bool pooled = p.slots != nullptr, packed = p.cu != nullptr;
+  const int rc = sizes_checked(p.B, p.T, p.D, p.G, p.N, packed, dtype);
+  if (rc == GDN_ERR_INVALID_ARG || (flags & ~GDN_SSM_SOFTPLUS)) return GDN_ERR_INVALID_ARG;
+  if (p.B > 0 && (!p.A_log || !p.hT || (p.T > 0 && (!p.x || !p.dt || !p.b || !p.c || !p.out))))
+    return GDN_ERR_INVALID_ARG;
+  if (rc != GDN_OK) return rc;
+  if (misaligned({p.x, p.dt, p.b, p.c, p.A_log, p.Dskip, p.z, p.dt_bias, p.h0, p.out, p.hT, workspace}, 16) ||
+      misaligned({p.cu, p.slots}, 4))
+    return GDN_ERR_INVALID_ARG;
+  Cut cut = cut_of(p.B, p.T, p.D, p.G, packed);
+  if (pooled) cut = Cut{true, std::max(p.T, 1), 1, 0};
+  const Space w = space_of(cut.segments, 0, 0, p.D, p.G, p.N, 1, false);
+  const long long need = cut.cut() ? w.bytes : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
+  p.rows = (packed ? 1LL : p.B) * (long long)p.T;
+  const long long e = dtype == GDN_BF16 ? 2 : 4, data = p.rows * p.D * e, keys = p.rows * p.G * p.N * e;
+  const long long state = (pooled ? p.nslots : p.B) * (long long)p.D * p.N * 4;
+  if (clash({{p.out, data}, {p.hT, state}, {need > 0 ? workspace : nullptr, need}},
+            {{p.x, data}, {p.dt, data}, {p.z, data}, {p.b, keys}, {p.c, keys}, {p.A_log, 4LL * p.D * p.N},
+             {p.Dskip, 4LL * p.D}, {p.dt_bias, 4LL * p.D}, {p.cu, 4LL * (p.B + 1)}, {p.slots, 4LL * p.B},
+             {p.h0 == p.hT ? nullptr : p.h0, state}}))
+    return GDN_ERR_INVALID_ARG;
+  if (p.B == 0) return GDN_OK;
+  p.Dg = p.D / p.G;
+  p.softplus = flags & GDN_SSM_SOFTPLUS;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool bf = dtype == GDN_BF16;
+  if (cut.recurrent) {
+    const long long wgs = (long long)p.B * tiles_of(p.D, 1024 / p.N);
+    if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
+    bf ? launch_recurrent<__bf16>(p, (unsigned)wgs, s) : launch_recurrent<float>(p, (unsigned)wgs, s);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  }
+  p.L = cut.L;
+  p.nseg = cut.nseg;
+  p.segments = cut.cut() ? cut.segments : slots_of(packed, p.B, p.T, p.L);
+  const long long wgs = p.segments * p.G * tiles_of(tiles_of(p.Dg, 64), 4);
+  const long long joins = std::min(MOST_WGS, ((long long)p.B * p.D * p.N + 255) / 256);
+  if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
+  if (cut.cut()) {
+    char* base = static_cast<char*>(workspace);
+    p.E = reinterpret_cast<float*>(base + w.E);
+    p.S = reinterpret_cast<float*>(base + w.S);
+    bf ? launch_outputs<__bf16>(p, (unsigned)wgs, false, s) : launch_outputs<float>(p, (unsigned)wgs, false, s);
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)joins), dim3(256), 0, s, p);
+  }
+  bf ? launch_outputs<__bf16>(p, (unsigned)wgs, true, s) : launch_outputs<float>(p, (unsigned)wgs, true, s);
+  return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" long long gdn_ssm_workspace_size(int B, int T, int D, int G, int N, int packed, int dtype, int backward) {
+  const int rc = sizes_checked(B, T, D, G, N, packed != 0, dtype);
+  if (rc != GDN_OK) return rc;
+  if (!backward) {
+    const Cut c = cut_of(B, T, D, G, packed != 0);
+    return c.cut() ? space_of(c.segments, 0, 0, D, G, N, 1, false).bytes : 0;
+  }
+  const BackPlan b = back_plan(B, T, D, G, N, packed != 0);
+  return space_of(b.segments, b.runs, b.rows, D, G, N, b.quads, true).bytes;
+}
+
+extern "C" int gdn_ssm_fwd(const void* x, const void* dt, const void* b, const void* c, const float* A_log,
+                           const float* Dskip, const void* z, const float* dt_bias, const float* h0,
+                           const int32_t* cu_seqlens, void* out, float* hT, int B, int T, int D, int G, int N,
+                           void* stream, int dtype, int flags, void* workspace, long long workspace_bytes) {
+  SsmParams p = {};
+  p.x = x; p.dt = dt; p.b = b; p.c = c; p.A_log = A_log; p.Dskip = Dskip; p.z = z; p.dt_bias = dt_bias;
+  p.h0 = h0; p.cu = cu_seqlens; p.out = out; p.hT = hT;
+  p.B = B; p.T = T; p.D = D; p.G = G; p.N = N;
+  return forward(p, dtype, flags, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gdn_ssm_fwd_recurrent_pool(const void* x, const void* dt, const void* b, const void* c,
+                                          const float* A_log, const float* Dskip, const void* z, const float* dt_bias,
+                                          float* pool, const int32_t* slots, const int32_t* cu_seqlens, void* out,
+                                          int nslots, int B, int T, int D, int G, int N, void* stream, int dtype,
+                                          int flags) {
+  if (nslots < 0 || (B > 0 && !slots)) return GDN_ERR_INVALID_ARG;
+  SsmParams p = {};
+  p.x = x; p.dt = dt; p.b = b; p.c = c; p.A_log = A_log; p.Dskip = Dskip; p.z = z; p.dt_bias = dt_bias;
+  p.h0 = pool; p.hT = pool; p.slots = slots; p.cu = cu_seqlens; p.out = out; p.nslots = nslots;
+  p.B = B; p.T = T; p.D = D; p.G = G; p.N = N;
+  return forward(p, dtype, flags, nullptr, 0, stream);
+}
+
+extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const void* c, const float* A_log,
+                           const float* Dskip, const void* z, const float* dt_bias, const float* h0,
+                           const int32_t* cu_seqlens, const void* dout, const float* dhT, void* dx, void* ddt, void* db,
+                           void* dc, float* dA_log, float* dD, void* dz, float* ddt_bias, float* dh0, int B, int T,
+                           int D, int G, int N, void* stream, int dtype, int flags, void* workspace,
+                           long long workspace_bytes) {
+  const bool packed = cu_seqlens != nullptr;
+  const int rc = sizes_checked(B, T, D, G, N, packed, dtype);
+  if (rc == GDN_ERR_INVALID_ARG || (flags & ~GDN_SSM_SOFTPLUS) || !A_log || !dA_log) return GDN_ERR_INVALID_ARG;
+  if (B > 0 && T > 0 && (!x || !dt || !b || !c || !dout || !dx || !ddt || !db || !dc)) return GDN_ERR_INVALID_ARG;
+  if (dz && !z) return GDN_ERR_INVALID_ARG;
+  if (rc != GDN_OK) return rc;
+  if (misaligned({x, dt, b, c, A_log, Dskip, z, dt_bias, h0, dout, dhT, dx, ddt, db, dc, dA_log, dD, dz, ddt_bias, dh0,
+                  workspace}, 16) || misaligned(cu_seqlens, 4))
+    return GDN_ERR_INVALID_ARG;
+  const BackPlan plan = back_plan(B, T, D, G, N, packed);
+  const Space w = space_of(plan.segments, plan.runs, plan.rows, D, G, N, plan.quads, true);
+  if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return GDN_ERR_INVALID_ARG;
+  const long long e = dtype == GDN_BF16 ? 2 : 4, data = plan.rows * D * e, keys = plan.rows * G * N * e;
+  const long long state = (long long)B * D * N * 4, rates = 4LL * D * N, vec = 4LL * D;
+  if (clash({{dx, data}, {ddt, data}, {db, keys}, {dc, keys}, {dA_log, rates}, {dD, vec}, {dz, data}, {ddt_bias, vec},
+             {dh0, state}, {workspace, w.bytes}},
+            {{x, data}, {dt, data}, {b, keys}, {c, keys}, {A_log, rates}, {Dskip, vec}, {z, data}, {dt_bias, vec},
+             {h0, state}, {cu_seqlens, 4LL * (B + 1)}, {dout, data}, {dh0 == dhT ? nullptr : dhT, state}}))
+    return GDN_ERR_INVALID_ARG;
+  SsmParams p = {};
+  p.x = x; p.dt = dt; p.b = b; p.c = c; p.A_log = A_log; p.Dskip = Dskip; p.z = z; p.dt_bias = dt_bias;
+  p.h0 = h0; p.cu = cu_seqlens; p.dout = dout; p.dhT = dhT; p.dx = dx; p.ddt = ddt; p.db = db; p.dc = dc;
+  p.dA_log = dA_log; p.dD = dD; p.dz = dz; p.ddt_bias = ddt_bias; p.dh0 = dh0;
+  char* base = static_cast<char*>(workspace);
+  p.E = reinterpret_cast<float*>(base + w.E);
+  p.R = reinterpret_cast<float*>(base + w.R);
+  p.S = reinterpret_cast<float*>(base + w.S);
+  p.keys = reinterpret_cast<float*>(base + w.keys);
+  p.sums = reinterpret_cast<float*>(base + w.sums);
+  p.B = B; p.T = T; p.D = D; p.G = G; p.N = N; p.Dg = D / G;
+  p.L = BL;
+  p.nseg = plan.nseg;
+  p.segments = plan.segments;
+  p.run = plan.run;
+  p.runs = (int)plan.runs;
+  p.rows = plan.rows;
+  p.softplus = flags & GDN_SSM_SOFTPLUS;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool bf = dtype == GDN_BF16;
+  const long long maps = std::min(MOST_WGS, (plan.segments * G * tiles_of(p.Dg, 64) * (N / 16) + 3) / 4);
+  const long long joins = std::min(MOST_WGS, ((long long)B * D * N + 255) / 256), wgs = plan.runs * G * plan.quads;
+  const long long cols = (long long)D * (N + 2);
+  if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
+  if (plan.segments > 0) {
+    if (bf) hipLaunchKernelGGL((ssm_bwd_maps_kernel<__bf16>), dim3((unsigned)maps), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((ssm_bwd_maps_kernel<float>), dim3((unsigned)maps), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)joins, 2), dim3(256), 0, s, p);
+    bf ? launch_bwd<__bf16>(p, (unsigned)wgs, s) : launch_bwd<float>(p, (unsigned)wgs, s);
+    if (plan.quads > 1 && plan.rows > 0) {
+      const long long total = plan.rows * G * 2 * N;
+      const unsigned grid = (unsigned)std::min<long long>(4096, (total + 255) / 256);
+      if (bf) hipLaunchKernelGGL((ssm_keys_kernel<__bf16>), dim3(grid), dim3(256), 0, s, p, plan.quads);
+      else hipLaunchKernelGGL((ssm_keys_kernel<float>), dim3(grid), dim3(256), 0, s, p, plan.quads);
+    }
+  }
+  hipLaunchKernelGGL(ssm_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, p);
+  return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}

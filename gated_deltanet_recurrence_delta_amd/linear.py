@@ -134,12 +134,12 @@ def _decays(g, H):
         raise ValueError("g is a constant of the model: it gets no gradient")
 
 
-def _scratch(need, workspace, dev, stream):
+def _scratch(need, workspace, dev, stream, size_call="gdn_linear_workspace_size"):
     """The call's workspace: the caller's, or one from the memory of the stream it runs on."""
     import torch
 
     if need < 0:
-        raise GdnError(need, strerror(need), "gdn_linear_workspace_size")
+        raise GdnError(need, strerror(need), size_call)
     if workspace is None:
         if need == 0:
             return None, 0

@@ -1,0 +1,369 @@
+"""The selective scan on the GPU against the FP64 oracle (tolerances:
+block_case.py)."""
+import numpy as np
+import pytest
+
+from block_case import check_ssm, check_ssm_bwd, f64
+
+torch = pytest.importorskip("torch")
+import gated_deltanet_recurrence_delta_amd as gdn  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+OPTIONS = ("D", "z", "dt_bias", "h0")
+
+
+def make(seed, dtype, lens, D, G, N, packed, without=(), steps=(1e-3, 0.5)):
+    r = np.random.default_rng(seed)
+    rows, B = sum(lens), len(lens)
+    dev = lambda a, t=torch.float32: torch.from_numpy(np.asarray(a, np.float32)).cuda().to(t)  # noqa: E731
+    lead = (rows,) if packed else (B, lens[0] if lens else 0)
+    step = np.exp(r.uniform(*np.log(steps), D))
+    t = {"x": dev(r.standard_normal((*lead, D)), DT[dtype]), "dt": dev(0.7 * r.standard_normal((*lead, D)), DT[dtype]),
+         "b": dev(r.standard_normal((*lead, G, N)), DT[dtype]), "c": dev(r.standard_normal((*lead, G, N)), DT[dtype]),
+         "A_log": dev(np.log(np.arange(1, N + 1)) + 0.2 * r.standard_normal((D, N))), "D": dev(r.standard_normal(D)),
+         "z": dev(r.standard_normal((*lead, D)), DT[dtype]), "dt_bias": dev(np.log(np.expm1(step))),
+         "h0": dev(r.standard_normal((B, D, N)))}
+    for n in without:
+        t[n] = None
+    t["cu_seqlens"] = torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32).cuda() if packed else None
+    c = {n: f64(t[n]) for n in ("A_log", "D", "dt_bias", "h0")}
+    for n in ("x", "dt", "b", "c", "z"):
+        c[n] = None if t[n] is None else f64(t[n]).reshape(rows, *((G, N) if n in "bc" else (D,)))
+    c["lens"] = lens
+    t["dout"], t["dhT"] = dev(r.standard_normal((*lead, D)), DT[dtype]), dev(r.standard_normal((B, D, N)))
+    c["dout"], c["dhT"] = f64(t["dout"]).reshape(rows, D), f64(t["dhT"])
+    return t, c
+
+
+def args(t):
+    return [t[n] for n in ("x", "dt", "b", "c", "A_log")], {n: t[n] for n in OPTIONS + ("cu_seqlens",)}
+
+
+def forward(t, **kw):
+    a, o = args(t)
+    return gdn.ssm_fwd(*a, **{**o, **kw})
+
+
+def backward(t, dhT=True, **kw):
+    a, o = args(t)
+    return gdn.ssm_bwd(*a, t["dout"], **o, dhT=t["dhT"] if dhT else None, **kw)
+
+
+def check_forward(t, c, dtype, soft=True):
+    out, hT = forward(t, softplus=soft)
+    check_ssm(c, f64(out).reshape(c["x"].shape), f64(hT), dtype, soft)
+
+
+def check_backward(t, c, dtype, soft=True, dhT=True):
+    g = backward(t, softplus=soft, dhT=dhT)
+    g = {n: None if v is None else f64(v).reshape(c[n[1:]].shape) if n[1:] in ("x", "dt", "b", "c", "z") else f64(v)
+         for n, v in g.items()}
+    check_ssm_bwd(c, g, c["dout"], c["dhT"] if dhT else None, dtype, soft)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [16, 32, 64])
+@pytest.mark.parametrize("T", [1, 2, 5, 31, 32, 33, 63, 65, 97, 200])
+def test_lengths_and_states(dtype, N, T):
+    t, c = make(N + T, dtype, [T] * 2, 72, 1, N, False)
+    check_forward(t, c, dtype)
+    check_backward(t, c, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G", [(1, 1), (7, 1), (64, 1), (65, 1), (130, 2), (96, 4), (12, 12), (300, 1), (520, 2)])
+@pytest.mark.parametrize("T", [9, 80])
+def test_channels_and_groups(dtype, D, G, T):
+    t, c = make(D + G, dtype, [T], D, G, 16 if D != 130 else 32, False)
+    check_forward(t, c, dtype)
+    check_backward(t, c, dtype)
+
+
+@pytest.mark.parametrize("without", [("D",), ("z",), ("dt_bias",), ("h0",), ("D", "z", "dt_bias", "h0")])
+@pytest.mark.parametrize("soft", [True, False])
+def test_options(without, soft):
+    t, c = make(5, "f32", [75] * 2, 40, 2, 16, False, without)
+    if not soft:
+        t["dt"].abs_().mul_(0.1)
+        c["dt"] = f64(t["dt"]).reshape(c["x"].shape)
+        if t["dt_bias"] is not None:
+            t["dt_bias"].abs_().mul_(0.01)
+            c["dt_bias"] = f64(t["dt_bias"])
+    check_forward(t, c, "f32", soft)
+    check_backward(t, c, "f32", soft, dhT="h0" not in without)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[5, 1, 0, 33, 64, 2], [0, 0, 70], [100, 3, 0], [1] * 90, [130, 0, 0, 0, 31]])
+def test_packed(dtype, lens):
+    t, c = make(len(lens), dtype, lens, 48, 2, 16, True)
+    check_forward(t, c, dtype)
+    check_backward(t, c, dtype)
+
+
+@pytest.mark.parametrize("N", [32, 64])
+def test_packed_wide_states(N):
+    t, c = make(N, "bf16", [77, 0, 3, 40], 50, 1, N, True)
+    check_forward(t, c, "bf16")
+    check_backward(t, c, "bf16")
+
+
+def test_enough_channels_for_no_cut():
+    """2,048 tiles of channels: sequences run as they are, and cut ones agree with them."""
+    T, B, D = 70, 2048, 8
+    assert gdn.gdn_ssm_workspace_size(B, T, D, 1, 16, 0, 1) == 0
+    t, c = make(1, "bf16", [T] * B, D, 1, 16, False)
+    out, hT = forward(t)
+    for n in (0, 1000, B - 1):
+        part = {k: v[n:n + 1] if k in ("x", "dt", "b", "c", "z", "h0") else v for k, v in t.items()}
+        one = {k: c[k] for k in ("A_log", "D", "dt_bias")}
+        one.update({k: c[k][n * T:(n + 1) * T] for k in ("x", "dt", "b", "c", "z")}, h0=c["h0"][n:n + 1], lens=[T])
+        check_ssm(one, f64(out[n]), f64(hT[n:n + 1]), "bf16", True)
+        check_forward(part, one, "bf16")
+
+
+def test_long_memories():
+    """Steps so small that a state outlives thousands of tokens, over many segments."""
+    t, c = make(2, "f32", [3000], 16, 1, 16, False, steps=(1e-6, 1e-4))
+    t["dt"].zero_()
+    c["dt"] *= 0
+    check_forward(t, c, "f32")
+    check_backward(t, c, "f32")
+
+
+def test_small_steps_keep_their_precision():
+    """softplus of large negative arguments: relative, not absolute."""
+    t, c = make(3, "f32", [4], 8, 1, 16, False, without=("dt_bias", "h0", "D", "z"))
+    for v in (-5.0, -12.0, -30.0, -60.0):
+        t["dt"].fill_(v)
+        c["dt"][:] = v
+        check_forward(t, c, "f32")
+
+
+def test_steps_so_large_that_nothing_is_left():
+    t, c = make(4, "f32", [70], 24, 1, 16, False, without=("dt_bias",))
+    t["dt"].fill_(200.0)
+    c["dt"][:] = 200.0
+    check_forward(t, c, "f32")
+    check_backward(t, c, "f32")
+
+
+@pytest.mark.parametrize("T", [30, 200])
+def test_rows_of_no_sequence_are_left(T):
+    t, c = make(6, "bf16", [T], 40, 1, 16, True)
+    lo, hi = 3, T - 5
+    t["cu_seqlens"] = torch.tensor([lo, lo, hi], dtype=torch.int32).cuda()
+    t["h0"], t["dhT"] = t["h0"].repeat(2, 1, 1), t["dhT"].repeat(2, 1, 1)
+    out = torch.full_like(t["x"], 77)
+    forward(t, out=out)
+    assert (out[:lo] == 77).all() and (out[hi:] == 77).all()
+    want = backward(t)
+    names = ("x", "dt", "b", "c", "A_log") + OPTIONS
+    for n in names:
+        t[n].requires_grad_()
+    a, o = args(t)
+    y, hT = gdn.selective_scan(*a, **o)
+    assert (y[:lo] == 0).all() and (y[hi:] == 0).all() and torch.equal(y[lo:hi], out[lo:hi])
+    grads = torch.autograd.grad([y, hT], [t[n] for n in names], [t["dout"], t["dhT"]])
+    for n, g in zip(names, grads):
+        if n in ("x", "dt", "b", "c", "z"):
+            assert (g[:lo] == 0).all() and (g[hi:] == 0).all() and torch.equal(g[lo:hi], want["d" + n][lo:hi]), n
+        else:
+            assert torch.equal(g, want["d" + n]), n
+
+
+def test_groups_of_several_workgroups_leave_rows():
+    """db and dc of a group whose channels are several workgroups' (a launch of their own)."""
+    t, c = make(7, "bf16", [60], 600, 1, 16, True)
+    t["cu_seqlens"] = torch.tensor([10, 50], dtype=torch.int32).cuda()
+    fill = torch.full_like(t["b"], 3)
+    grads = {}
+    a, o = args(t)
+    from gated_deltanet_recurrence_delta_amd import ssm
+    real, torch_empty = ssm._call, {}
+
+    def call(name, dev, *p):  # fills db and dc before they are written
+        for q in torch_empty["k"]:
+            q.copy_(fill)
+        return real(name, dev, *p)
+
+    like = torch.empty_like
+
+    def empty_like(x, **k):
+        y = like(x, **k)
+        if x.shape == fill.shape:
+            torch_empty.setdefault("k", []).append(y)
+        return y
+
+    torch.empty_like, ssm._call = empty_like, call
+    try:
+        grads = gdn.ssm_bwd(*a, t["dout"], **o)
+    finally:
+        torch.empty_like, ssm._call = like, real
+    for n in ("db", "dc"):
+        assert (grads[n][:10] == 3).all() and (grads[n][50:] == 3).all() and (grads[n][10:50] != 3).any()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_in_place_states(T):
+    t, _ = make(8, "bf16", [T] * 2, 72, 1, 16, False)
+    out, hT = forward(t)
+    h = t["h0"].clone()
+    o, h2 = forward(t, h0=h, hT=h)
+    assert h2 is h and torch.equal(o, out) and torch.equal(h, hT)
+
+
+def test_split_sequences():
+    """A sequence's second part from the first one's state."""
+    t, c = make(9, "f32", [150], 32, 1, 16, False)
+    a, o = args(t)
+    cut = lambda s: ([v[:, s].contiguous() if v.dim() > 2 else v for v in a],  # noqa: E731
+                     {**o, "z": o["z"][:, s].contiguous()})
+    a1, o1 = cut(slice(0, 80))
+    a2, o2 = cut(slice(80, 150))
+    out1, h1 = gdn.ssm_fwd(*a1, **o1)
+    out2, h2 = gdn.ssm_fwd(*a2, **{**o2, "h0": h1})
+    check_ssm(c, f64(torch.cat([out1, out2], 1))[0], f64(h2), "f32", True)
+
+
+def test_no_tokens():
+    t, c = make(10, "f32", [0, 0], 24, 1, 16, True)
+    out, hT = forward(t)
+    assert torch.equal(hT, t["h0"])
+    g = backward(t)
+    assert torch.equal(g["dh0"], t["dhT"])
+    assert not g["dA_log"].any() and not g["dD"].any() and not g["ddt_bias"].any()
+    a, o = args(t)
+    g = gdn.ssm_bwd(*a, t["dout"], **{**o, "cu_seqlens": t["cu_seqlens"][:1], "h0": None})
+    assert not g["dA_log"].any() and g["dh0"].shape[0] == 0
+
+
+def test_non_finite_values_stay_with_their_channel():
+    t, _ = make(11, "f32", [90], 20, 1, 16, False)
+    out, hT = forward(t)
+    for n, bad in (("x", float("nan")), ("z", float("inf")), ("dt", float("nan"))):
+        u = {**t, n: t[n].clone()}
+        u[n][0, 40, 7] = bad
+        o, h = forward(u)
+        rest = torch.arange(20, device="cuda") != 7
+        assert torch.equal(o[..., rest], out[..., rest]) and torch.equal(h[:, rest], hT[:, rest]), n
+        assert not torch.equal(o[0, 40:, 7], out[0, 40:, 7])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,D,G,N", [(1, 1, 64, 1, 16), (5, 1, 1280, 1, 16), (3, 4, 33, 3, 32), (70, 1, 8, 2, 64),
+                                       (2, 90, 40, 1, 16)])
+def test_pool(dtype, B, T, D, G, N):
+    t, c = make(B, dtype, [T] * B, D, G, N, False)
+    r = np.random.default_rng(B)
+    pool = torch.from_numpy(r.standard_normal((B + 5, D, N)).astype(np.float32)).cuda()
+    slots = torch.from_numpy(r.permutation(B + 5)[:B].astype(np.int32)).cuda()
+    before = pool.clone()
+    c["h0"] = f64(before[slots.long()])
+    a, o = args(t)
+    o = {k: o[k] for k in ("D", "z", "dt_bias")}
+    out = gdn.ssm_fwd_recurrent_pool(*a, pool, slots, **o)
+    check_ssm(c, f64(out).reshape(B * T, D), f64(pool[slots.long()]), dtype, True)
+    rest = torch.ones(B + 5, dtype=torch.bool)
+    rest[slots.long().cpu()] = False
+    assert torch.equal(pool[rest.cuda()], before[rest.cuda()])
+    # packed: the same
+    other = before.clone()
+    cu = torch.arange(0, B * T + 1, T, dtype=torch.int32).cuda()
+    flat = lambda v: v.reshape(B * T, *v.shape[2:])  # noqa: E731
+    p = gdn.ssm_fwd_recurrent_pool(*[flat(v) for v in a[:4]], a[4], other, slots, D=o["D"], z=flat(o["z"]),
+                                   dt_bias=o["dt_bias"], cu_seqlens=cu)
+    assert torch.equal(p, flat(out)) and torch.equal(other, pool)
+
+
+def test_pool_bad_slots():
+    t, c = make(12, "bf16", [2] * 5, 64, 1, 16, False)
+    pool = torch.randn(6, 64, 16, device="cuda")
+    a, o = args(t)
+    o = {k: o[k] for k in ("D", "z", "dt_bias")}
+    want_pool = pool.clone()
+    want = gdn.ssm_fwd_recurrent_pool(*[v[:1] for v in a[:4]], a[4], want_pool, torch.tensor([4], dtype=torch.int32).cuda(),
+                                      D=o["D"], z=o["z"][:1], dt_bias=o["dt_bias"])
+    bad = torch.tensor([4, -1, 4, 6, 2 ** 31 - 1], dtype=torch.int32).cuda()
+    out = gdn.ssm_fwd_recurrent_pool(*a, pool, bad, **o)
+    assert torch.equal(out[:1], want) and not out[1:].any() and torch.equal(pool, want_pool)
+
+
+def test_captured_step_takes_each_replay_s_inputs():
+    t, c = make(13, "bf16", [1] * 3, 64, 1, 16, False)
+    pool = torch.randn(4, 64, 16, device="cuda")
+    slots = torch.tensor([2, 0, 3], dtype=torch.int32).cuda()
+    a, o = args(t)
+    o = {k: o[k] for k in ("D", "z", "dt_bias")}
+    ref_pool, out = pool.clone(), torch.empty_like(t["x"])
+    gdn.ssm_fwd_recurrent_pool(*a, pool.clone(), slots, **o, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.ssm_fwd_recurrent_pool(*a, pool, slots, **o, out=out)
+    for i in range(4):
+        t["x"].copy_(torch.randn(t["x"].shape, generator=torch.Generator().manual_seed(i)).cuda())
+        slots.copy_(torch.roll(slots, 1))
+        torch.cuda.synchronize()
+        graph.replay()
+        want = gdn.ssm_fwd_recurrent_pool(*a, ref_pool, slots, **o)
+        assert torch.equal(out, want) and torch.equal(pool, ref_pool)
+
+
+def test_captured_training_step():
+    """Forwards and backwards of a packed batch in a graph whose offsets change between replays."""
+    t, _ = make(14, "bf16", [70, 50, 80], 64, 1, 16, True)
+    offsets = [[0, 70, 120, 200], [0, 0, 199, 200], [0, 100, 101, 200], [0, 200, 200, 200]]
+    forward(t), backward(t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, hT = forward(t)
+        g = backward(t)
+    for o in offsets:
+        t["cu_seqlens"].copy_(torch.tensor(o, dtype=torch.int32))
+        t["x"].mul_(-1.25)
+        torch.cuda.synchronize()
+        graph.replay()
+        w, wh = forward(t)
+        wg = backward(t)
+        assert torch.equal(out, w) and torch.equal(hT, wh)
+        assert all(torch.equal(g[n], wg[n]) for n in g), o
+
+
+def test_another_stream():
+    t, _ = make(15, "bf16", [150, 9], 64, 1, 16, True)
+    want, g = forward(t), backward(t)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out, hT = forward(t, stream=stream)
+    g2 = backward(t, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(hT, want[1])
+    assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("offsets", [[0, 90, 40, 120], [5, 3, 999, -7], [120, 0, 0, 0], [-5, 400, 400, 400]])
+def test_offsets_outside_or_falling_stay_inside_the_tensors(offsets):
+    t, _ = make(16, "f32", [120], 64, 1, 16, True)
+    t["cu_seqlens"] = torch.tensor(offsets, dtype=torch.int32).cuda()
+    t["h0"], t["dhT"] = t["h0"].repeat(3, 1, 1), t["dhT"].repeat(3, 1, 1)
+    whole, states = torch.full((3, 120, 64), 7.0, device="cuda"), torch.full((5, 64, 16), 7.0, device="cuda")
+    need = gdn.gdn_ssm_workspace_size(3, 120, 64, 1, 16, 1, 0)
+    ws = torch.full((3, need), 7, dtype=torch.uint8, device="cuda")
+    forward(t, out=whole[1], hT=states[1:4], workspace=ws[1])
+    assert (whole[0] == 7).all() and (whole[2] == 7).all() and (states[0] == 7).all() and (states[4] == 7).all()
+    assert (ws[0] == 7).all() and (ws[2] == 7).all()
+    need = gdn.gdn_ssm_workspace_size(3, 120, 64, 1, 16, 1, 0, 1)
+    ws = torch.full((3, need), 7, dtype=torch.uint8, device="cuda")
+    backward(t, workspace=ws[1])
+    assert (ws[0] == 7).all() and (ws[2] == 7).all()
+
+
+def test_twice_the_same():
+    t, _ = make(17, "f32", [300, 41], 96, 1, 32, True)
+    a, b = forward(t), forward(t)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    a, b = backward(t), backward(t)
+    assert all(torch.equal(a[n], b[n]) for n in a)
