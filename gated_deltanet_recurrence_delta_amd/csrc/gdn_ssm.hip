@@ -75,10 +75,13 @@ __device__ static inline float softplus(float v) {
   y = __builtin_fmaf(w, y, 0.400245965f);
   y = __builtin_fmaf(w, y, 0.666663229f);
   y = __builtin_fmaf(w, y, 2.f);
-  return __builtin_fmaf(q, y, v > 0.f ? v : v - v);  // v - v: 0, and NaN for a NaN
+  return __builtin_fmaf(q, y, __builtin_fmaxf(v, 0.f));
 }
 
-__device__ static inline float step_of(float v, int soft) { return soft ? softplus(v) : v; }
+__device__ static inline float step_of(float v, int soft) {
+  const float s = softplus(v);  // no branch
+  return soft ? s : v;
+}
 
 // -------------------------------------------------------------------- keys --
 
@@ -92,6 +95,10 @@ struct Keys16 {
   __device__ void load(const TI* p) {
     w = *(const __attribute__((address_space(4))) words*)(uintptr_t)p;
   }
+  // Makes the loaded values be there at this point of the instruction stream.
+  // Scalar loads return in any order, so that a wait for one is a wait for all:
+  // the next ones are to be issued behind it.
+  __device__ void arrive() { asm volatile("" : "+s"(w)); }
   __device__ float operator[](int i) const {
     // (a value first: a bit cast of a vector's element itself took element 0)
     const uint32_t u = sizeof(TI) == 4 ? w[i] : i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16;
@@ -112,22 +119,17 @@ struct Place {
   bool active;  // the lane's channel is one of the group's
 };
 
-// Waves of a workgroup take neighbouring tiles of 64 channels.
+// A workgroup is one wave: no wave waits for another, and any number of tiles is
+// spread evenly.
 __device__ static inline Place place_of(const SsmParams& p) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = (p.Dg + 63) >> 6, quads = (tiles + 3) >> 2;
+  const int lane = threadIdx.x & 63, tiles = (p.Dg + 63) >> 6;
   Place w;
   int k = blockIdx.x;
-  const int tile = k % quads * 4 + wave;
-  k /= quads;
+  const int c = k % tiles * 64 + lane;
+  k /= tiles;
   w.g = k % p.G;
   w.slot = k / p.G;
-  if (tile >= tiles) {
-    w.s.n = -1;
-    return w;
-  }
   w.s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, w.slot);
-  const int c = tile * 64 + lane;
   w.active = c < p.Dg;
   w.d = w.g * p.Dg + min(c, p.Dg - 1);
   return w;
@@ -149,16 +151,63 @@ __device__ static inline void store_states(float* p, const Vals<N>& h) {
   for (int i = 0; i < N; i += 4) store_vals<float, 4>(p + i, Vals<4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}});
 }
 
+template <int BYTES>
+struct Bits {
+  typedef uint32_t type;
+};
+template <>
+struct Bits<2> {
+  typedef uint16_t type;
+};
+
+// Sixteen of a token's write and read keys.
+template <typename TI, bool READ>
+struct KeyPair {
+  Keys16<TI> b, c;
+  __device__ void load(const TI* bk, const TI* ck) {
+    b.load(bk);
+    if constexpr (READ) c.load(ck);
+  }
+  __device__ void arrive() {
+    b.arrive();
+    if constexpr (READ) c.arrive();
+  }
+};
+
+// A lane's value in a row of one of the token tensors.  The row's address, the
+// same in all lanes, is kept in scalar registers (the assembly is empty; without
+// it the sum is formed in vector registers, three instructions a load), and the
+// value in 32 bits (two of 16 would be packed, and waited for, on the way).
+template <typename TI>
+struct Row {
+  typedef typename Bits<sizeof(TI)>::type bits;
+  typedef __attribute__((address_space(1))) bits* place;
+  __device__ static place at(const TI* row, uint32_t& lane) {
+    uintptr_t a = reinterpret_cast<uintptr_t>(row);
+    asm("" : "+s"(a), "+v"(lane));
+    return (place)((__attribute__((address_space(1))) char*)a + lane);
+  }
+  __device__ static uint32_t load(const TI* row, uint32_t& lane) { return *at(row, lane); }
+  __device__ static void store(TI* row, uint32_t& lane, float x) { *at(row, lane) = __builtin_bit_cast(bits, (TI)x); }
+  // Of the lanes whose place is inside the row of `bytes` bytes, without a branch.
+  __device__ static void store_inside(TI* row, int bytes, uint32_t lane, float x) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(row, 0, bytes, 0x00020000);
+    const bits b = __builtin_bit_cast(bits, (TI)x);
+    if constexpr (sizeof(TI) == 2) __builtin_amdgcn_raw_buffer_store_b16(b, r, lane, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(b, r, lane, 0, 0);
+  }
+  __device__ static float widen(uint32_t x) { return __builtin_bit_cast(float, sizeof(TI) == 2 ? x << 16 : x); }
+};
+
 // Forwards.  OUTPUT: the outputs from the segment's start state (E if the
 // sequences are cut, else h0).  Otherwise the state that a segment leaves from
 // zero, and the sum of its steps; what follows the last segment is hT, which
 // the outputs' launch gives.
 template <typename TI, int N, bool OUTPUT>
-__global__ __launch_bounds__(256) void ssm_kernel(const SsmParams p) {
+__global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
   const Place w = place_of(p);
-  if (w.s.n < 0 || (!OUTPUT && w.s.last())) return;
+  if (w.s.n < 0 || (!OUTPUT && w.s.last()) || !w.active) return;
   const int D = p.D, d = w.d;
-  const long KS = (long)p.G * N;
   Vals<N> A, h;
   load_states<N>(A, p.A_log + (long)d * N);
 #pragma unroll
@@ -171,74 +220,74 @@ __global__ __launch_bounds__(256) void ssm_kernel(const SsmParams p) {
     else if (p.h0) load_states<N>(h, p.h0 + ((long)w.s.n * D + d) * N);
   }
   const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = OUTPUT && p.Dskip ? p.Dskip[d] : 0.f;
-  const long at = w.s.row0 * D + d;
+  uint32_t lane = (uint32_t)d * sizeof(TI);
+  const long at = w.s.row0 * D;
   const TI* x = static_cast<const TI*>(p.x) + at;
   const TI* dt = static_cast<const TI*>(p.dt) + at;
-  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
-  TI* out = static_cast<TI*>(p.out) + at;
-  const TI* bk = static_cast<const TI*>(p.b) + (w.s.row0 * p.G + w.g) * N;
-  const TI* ck = static_cast<const TI*>(p.c) + (w.s.row0 * p.G + w.g) * N;
+  const TI* z = (p.z ? static_cast<const TI*>(p.z) : static_cast<const TI*>(p.x)) + at;
+  TI* out = static_cast<TI*>(p.out) + (OUTPUT ? at : 0);
   const int len = w.s.len;
   float S = 0.f;
 
-  TI xn[FLIGHT], dn[FLIGHT], zn[FLIGHT];
-#pragma unroll
-  for (int f = 0; f < FLIGHT; ++f) {
-    const long o = (long)min(f, max(len - 1, 0)) * D;
-    if (len > 0) {
-      xn[f] = x[o];
-      dn[f] = dt[o];
-      if (OUTPUT) zn[f] = z[o];
-    }
-  }
-  Keys16<TI> bn, cn;
   if (len > 0) {
-    bn.load(bk);
-    if (OUTPUT) cn.load(ck);
-  }
-  for (int t = 0; t < len; t += FLIGHT) {
-    TI xr[FLIGHT], dr[FLIGHT], zr[FLIGHT];
+    uint32_t xn[FLIGHT], dn[FLIGHT], zn[FLIGHT];
 #pragma unroll
     for (int f = 0; f < FLIGHT; ++f) {
-      xr[f] = xn[f];
-      dr[f] = dn[f];
-      if (OUTPUT) zr[f] = zn[f];
-      const long o = (long)min(t + FLIGHT + f, len - 1) * D;
-      xn[f] = x[o];
-      dn[f] = dt[o];
-      if (OUTPUT) zn[f] = z[o];
+      const long o = (long)min(f, len - 1) * D;
+      xn[f] = Row<TI>::load(x + o, lane);
+      dn[f] = Row<TI>::load(dt + o, lane);
+      if (OUTPUT) zn[f] = Row<TI>::load(z + o, lane);
     }
+    // The keys of the next sixteen states are on their way while these are
+    // worked on: two sets, taken in turn.
+    const long KS = (long)p.G * N;
+    const TI* bk = static_cast<const TI*>(p.b) + (w.s.row0 * p.G + w.g) * N;
+    const TI* ck = static_cast<const TI*>(p.c) + (w.s.row0 * p.G + w.g) * N;
+    KeyPair<TI, OUTPUT> keys[2];
+    keys[0].load(bk, ck);
+    for (int t = 0; t < len; t += FLIGHT) {
+      // Tokens behind the segment's last take a step of zero: the states stay.
+      // (No branch on the way, or what is to be in flight sinks below it: tokens
+      // behind the last store the last one's output once more.)
+      float y_last = 0.f;
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      if (t + f >= len) break;
-      const float xv = (float)xr[f], s = step_of((float)dr[f] + bias, p.softplus), u = s * xv;
-      float y = 0.f;
-      if constexpr (!OUTPUT) S += s;
+      for (int f = 0; f < FLIGHT; ++f) {
+        const float xv = Row<TI>::widen(xn[f]), v = Row<TI>::widen(dn[f]) + bias, soft = softplus(v);
+        const float zv = OUTPUT ? Row<TI>::widen(zn[f]) : 0.f;
+        const long o = (long)min(t + FLIGHT + f, len - 1) * D;
+        xn[f] = Row<TI>::load(x + o, lane);
+        dn[f] = Row<TI>::load(dt + o, lane);
+        if (OUTPUT) zn[f] = Row<TI>::load(z + o, lane);
+        const float s = t + f < len ? p.softplus ? soft : v : 0.f, u = s * xv;
+        float y = 0.f;
+        if constexpr (!OUTPUT) S += s;
 #pragma unroll
-      for (int n = 0; n < N; n += 16) {
-        const Keys16<TI> bv = bn, cv = cn;
-        // the next sixteen
-        const long next = n + 16 < N ? (long)(t + f) * KS + n + 16 : (long)min(t + f + 1, len - 1) * KS;
-        bn.load(bk + next);
-        if (OUTPUT) cn.load(ck + next);
+        for (int n = 0; n < N; n += 16) {
+          KeyPair<TI, OUTPUT>&now = keys[(f * (N / 16) + n / 16) & 1], &next = keys[(f * (N / 16) + n / 16 + 1) & 1];
+          // (behind the last token: its own again)
+          const long step = n + 16 < N ? 16 : (t + f + 1 < len ? KS : 0) - (N - 16);
+          bk += step;
+          ck += step;
+          now.arrive();
+          __builtin_amdgcn_sched_barrier(0);
+          next.load(bk, ck);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = __builtin_amdgcn_exp2f(s * A[n + i]);
-          h[n + i] = __builtin_fmaf(a, h[n + i], u * bv[i]);
-          if constexpr (OUTPUT) y = __builtin_fmaf(cv[i], h[n + i], y);
+          for (int i = 0; i < 16; ++i) {
+            const float a = __builtin_amdgcn_exp2f(s * A[n + i]);
+            h[n + i] = __builtin_fmaf(a, h[n + i], u * now.b[i]);
+            if constexpr (OUTPUT) y = __builtin_fmaf(now.c[i], h[n + i], y);
+          }
         }
-      }
-      if constexpr (OUTPUT) {
-        y = __builtin_fmaf(skip, xv, y);
-        if (p.z) {
-          const float zv = (float)zr[f];
-          y *= zv * sigmoid(zv);
+        if constexpr (OUTPUT) {
+          const float gate = zv * sigmoid(zv);
+          y = __builtin_fmaf(skip, xv, y) * (p.z ? gate : 1.f);
+          y_last = t + f < len ? y : y_last;
+          Row<TI>::store(out + (long)min(t + f, len - 1) * D, lane, y_last);
         }
-        if (w.active) out[(long)(t + f) * D] = (TI)y;
       }
     }
   }
-  if (!w.active) return;
   if constexpr (OUTPUT) {
     if (w.s.last()) store_states<N>(p.hT + ((long)w.s.n * D + d) * N, h);
   } else {
@@ -247,121 +296,195 @@ __global__ __launch_bounds__(256) void ssm_kernel(const SsmParams p) {
   }
 }
 
-// Joins the segments of each sequence: a thread is one state.  Forwards E, the
-// state each segment leaves from zero, becomes the one it starts from;
-// backwards in time R, likewise, for the state's gradient (blockIdx.y == 1).
-__device__ static inline void join_state(const SsmParams& p, long DN, long id, bool back) {
-  const int n = (int)(id / DN);
-  const long r = id - n * DN;
-  const int d = (int)(r / p.N);
-  long slot = (long)n * p.nseg;
-  int count = p.nseg;
-  if (p.cu) {
-    const int b = taken(p.cu[n], 0, p.T), e = taken(p.cu[n + 1], b, p.T);
-    slot = b / p.L + n;
-    count = (int)min((long)(e - b + p.L - 1) / p.L, max(p.segments - slot, 0L));
-  } else if (p.T == 0) {
-    count = 0;
-  }
-  const float A = -LOG2E * expf(p.A_log[r]);
-  float* state = (back ? p.R : p.E) + r;
-  const float* first = back ? p.dhT : p.h0;
-  float h = first ? first[id] : 0.f;
-  constexpr int F = 8;  // segments on their way at once
-  for (int i = 0; i < count; i += F) {
-    float e[F], s[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const long k = slot + (back ? count - 1 - min(i + f, count - 1) : min(i + f, count - 1));
-      e[f] = state[k * DN];
-      s[f] = p.S[k * p.D + d];
-    }
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-      if (i + f < count) {
-        const long k = slot + (back ? count - 1 - (i + f) : i + f);
-        state[k * DN] = h;
-        // the last segment's own state is not needed forwards, nor formed where outputs are
-        h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * s[f]), h, e[f]);
-      }
-  }
-  if (back) {
-    if (p.dh0) p.dh0[id] = h;
-  } else if (count == 0) {
-    p.E[((long)(p.cu ? taken(p.cu[n], 0, p.T) / p.L + n : slot)) * DN + r] = h;  // an empty sequence's one segment
-  }
-}
-
+// Joins the segments of each sequence, a thread for each state and each of
+// GROUPS parts of its segments: the parts are folded, then walked from the
+// state that the ones before leave.  Forwards E, the state each segment leaves
+// from zero, becomes the one it starts from; backwards in time R, likewise, for
+// the state's gradient (blockIdx.y == 1).
+//
+// Bound by the latency of a chain of loads: 200 segments of 20,480 states take
+// 25 us in one part.
+template <int GROUPS>
 __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
+  constexpr int STATES = 256 / GROUPS, F = 16;  // segments on their way at once
+  __shared__ float ends[GROUPS][STATES], sums[GROUPS][STATES];
   const long DN = (long)p.D * p.N;
-  for (long id = (long)blockIdx.x * 256 + threadIdx.x; id < p.B * DN; id += (long)gridDim.x * 256)
-    join_state(p, DN, id, blockIdx.y);
+  const int lane = threadIdx.x % STATES, group = threadIdx.x / STATES;
+  const bool back = blockIdx.y;
+  for (long id0 = (long)blockIdx.x * STATES; id0 < p.B * DN; id0 += (long)gridDim.x * STATES) {
+    const long id = min(id0 + lane, p.B * DN - 1);
+    const int n = (int)(id / DN);
+    const long r = id - n * DN;
+    const int d = (int)(r / p.N);
+    long slot = (long)n * p.nseg;
+    int count = p.T > 0 ? p.nseg : 0;
+    if (p.cu) {
+      const int b = taken(p.cu[n], 0, p.T), e = taken(p.cu[n + 1], b, p.T);
+      slot = b / p.L + n;
+      count = (int)min((long)(e - b + p.L - 1) / p.L, max(p.segments - slot, 0L));
+    }
+    const float A = -LOG2E * expf(p.A_log[r]);
+    float* state = (back ? p.R : p.E) + r;
+    const float* first = back ? p.dhT : p.h0;
+    const int part = (count + GROUPS - 1) / GROUPS, i0 = min(group * part, count), i1 = min(i0 + part, count);
+    const long step = back ? -1 : 1, begin = back ? slot + count - 1 : slot;
+    float h = 0.f, e[F], s[F];
+    auto load = [&](int i) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const long k = begin + step * min(i + f, i1 - 1);
+        e[f] = state[k * DN];
+        s[f] = p.S[k * p.D + d];
+      }
+    };
+    if constexpr (GROUPS > 1) {
+      float S = 0.f;
+      for (int i = i0; i < i1; i += F) {
+        load(i);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          if (i + f < i1) {
+            h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * s[f]), h, e[f]);
+            S += s[f];
+          }
+      }
+      __syncthreads();  // the sums of the states before have been read
+      ends[group][lane] = h;
+      sums[group][lane] = S;
+      __syncthreads();
+    }
+    h = first ? first[id] : 0.f;
+    if constexpr (GROUPS > 1)
+      for (int g = 0; g < group; ++g) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * sums[g][lane]), h, ends[g][lane]);
+    if (id0 + lane >= p.B * DN) continue;
+    for (int i = i0; i < i1; i += F) {
+      load(i);
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        if (i + f < i1) {
+          state[(begin + step * (i + f)) * DN] = h;
+          // a forward call's last segment has no state of its own here, and none is needed
+          h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * s[f]), h, e[f]);
+        }
+    }
+    if (group != GROUPS - 1) continue;
+    if (back) {
+      if (p.dh0) p.dh0[id] = h;
+    } else if (count == 0) {
+      p.E[slot * DN + r] = h;  // an empty sequence's one segment
+    }
+  }
 }
 
 // --------------------------------------------------------- token by token --
 
+template <int J>
+__device__ static inline float from_quad(float x) {
+  return dpp<J * 0x55>(x);
+}
+
+__device__ static inline Vals<4> quad(float x) {
+  return {{from_quad<0>(x), from_quad<1>(x), from_quad<2>(x), from_quad<3>(x)}};
+}
+
+// Four sums over a quad's lanes: lane j gets the j-th, over all LC lanes where
+// that is more than four.
+template <int LC>
+__device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
+  const float a = (odd ? v[1] : v[0]) + dpp<0xB1>(odd ? v[0] : v[1]);
+  const float b = (odd ? v[3] : v[2]) + dpp<0xB1>(odd ? v[2] : v[3]);
+  float r = (high ? b : a) + dpp<0x4E>(high ? a : b);
+  if constexpr (LC == 8) r += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(r), (4 << 10) | 0x1f));
+  if constexpr (LC == 16) {
+    r += dpp<0x128>(r);  // row_ror 8
+    r += dpp<0x124>(r);  // row_ror 4
+  }
+  return r;
+}
+
 // Few tokens on states read and written once: a lane holds four neighbouring
 // states (16 bytes), so that a wave's accesses cover whole lines; N / 4 lanes
-// are a channel.
-template <typename TI, int N>
+// are a channel.  Tokens are taken four a turn: lane 4 i + j forms the step and
+// gate of the turn's token j and writes its output, and what the others need of
+// them comes by DPP, so that a token costs a lane some 45 instructions, not 95.
+// TURNS turns are on their way at once.
+//
+// Bound by memory for one token each (X us, Y floor: 128 sequences, 1,280
+// channels); for longer sequences of few channels by one wave's instructions.
+template <typename TI, int N, int TURNS>
 __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
   constexpr int LC = N / 4, CH = 256 / LC;
   const int tiles = (p.D + CH - 1) / CH;
   const int n = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int lane = threadIdx.x % LC, d0 = tile * CH + threadIdx.x / LC;
+  const int slice = threadIdx.x % LC, d = tile * CH + threadIdx.x / LC, own = slice & 3;
+  const bool odd = slice & 1, high = slice & 2;
   const Segment s = sequence_of(p.cu, p.T, n);
   int state = n;
   if (p.slots) state = pool_slot(p.slots, p.nslots, n);
-  if (d0 >= p.D) return;
-  const int D = p.D, d = d0;
-  const long at = s.row0 * D + d;
-  TI* out = static_cast<TI*>(p.out) + at;
+  if (d >= p.D) return;
+  const int D = p.D, len = s.len;
+  TI* out = static_cast<TI*>(p.out) + s.row0 * D + d;
   if (state < 0) {
-    if (lane == 0)
-      for (int t = 0; t < s.len; ++t) out[(long)t * D] = (TI)0.f;
+    for (int t = slice; t < len; t += LC) out[(long)t * D] = (TI)0.f;
     return;
   }
-  const long sat = ((long)state * D + d) * N + lane * 4;
-  Vals<4> h = {{0.f, 0.f, 0.f, 0.f}}, A = load_vals<float, 4>(p.A_log + (long)d * N + lane * 4);
+  const long sat = ((long)state * D + d) * N + slice * 4;
+  Vals<4> h = {{0.f, 0.f, 0.f, 0.f}}, A = load_vals<float, 4>(p.A_log + (long)d * N + slice * 4);
   if (p.h0) h = load_vals<float, 4>(p.h0 + sat);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = -LOG2E * expf(A[i]);
   const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.Dskip ? p.Dskip[d] : 0.f;
-  const TI* x = static_cast<const TI*>(p.x) + at;
-  const TI* dt = static_cast<const TI*>(p.dt) + at;
-  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
-  const long key = (s.row0 * p.G + d / p.Dg) * N + lane * 4, KS = (long)p.G * N;
+  const TI* x = static_cast<const TI*>(p.x) + s.row0 * D + d;
+  const TI* dt = static_cast<const TI*>(p.dt) + s.row0 * D + d;
+  const TI* z = p.z ? static_cast<const TI*>(p.z) + s.row0 * D + d : x;
+  const long key = (s.row0 * p.G + d / p.Dg) * N + slice * 4, KS = (long)p.G * N;
   const TI* bk = static_cast<const TI*>(p.b) + key;
   const TI* ck = static_cast<const TI*>(p.c) + key;
-  TI xn = {}, dn = {}, zn = {};
-  typename Raw<TI, 4>::type bn = {}, cn = {};
-  if (s.len > 0) {
-    xn = x[0];
-    dn = dt[0];
-    zn = z[0];
-    bn = load_raw<TI, 4>(bk);
-    cn = load_raw<TI, 4>(ck);
-  }
-  for (int t = 0; t < s.len; ++t) {
-    const float xv = (float)xn, v = (float)dn + bias, zv = (float)zn;
-    const Vals<4> b = widen<TI, 4>(bn), c = widen<TI, 4>(cn);
-    const int f = min(t + 1, s.len - 1);
-    xn = x[(long)f * D];
-    dn = dt[(long)f * D];
-    zn = z[(long)f * D];
-    bn = load_raw<TI, 4>(bk + f * KS);
-    cn = load_raw<TI, 4>(ck + f * KS);
-    const float st = step_of(v, p.softplus), u = st * xv;
-    float y = 0.f;
+  TI xn[TURNS], dn[TURNS], zn[TURNS];
+  typename Raw<TI, 4>::type bn[TURNS][4], cn[TURNS][4];
+  auto load = [&](int k, int t) {
+    const long o = (long)min(t + own, len - 1) * D;
+    xn[k] = x[o];
+    dn[k] = dt[o];
+    zn[k] = z[o];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(st * A[i]), h[i], u * b[i]);
-      y = __builtin_fmaf(c[i], h[i], y);
+    for (int f = 0; f < 4; ++f)
+      if (t + f < len) {
+        bn[k][f] = load_raw<TI, 4>(bk + (t + f) * KS);
+        cn[k][f] = load_raw<TI, 4>(ck + (t + f) * KS);
+      }
+  };
+#pragma unroll
+  for (int k = 0; k < TURNS; ++k)
+    if (4 * k < len) load(k, 4 * k);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = -LOG2E * expf(A[i]);
+  for (int t0 = 0; t0 < len; t0 += 4 * TURNS)
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) {
+      const int t = t0 + 4 * k;
+      if (t >= len) break;
+      const float xv = (float)xn[k], zv = (float)zn[k];
+      const float st = step_of((float)dn[k] + bias, p.softplus);
+      const Vals<4> sv = quad(st), uv = quad(st * xv);
+      Vals<4> b[4], c[4], y = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        b[f] = widen<TI, 4>(bn[k][f]);
+        c[f] = widen<TI, 4>(cn[k][f]);
+      }
+      if (t + 4 * TURNS < len) load(k, t + 4 * TURNS);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if (t + f >= len) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[f] * A[i]), h[i], uv[f] * b[f][i]);
+          y[f] = __builtin_fmaf(c[f][i], h[i], y[f]);
+        }
+      }
+      float o = __builtin_fmaf(skip, xv, sum_own<LC>(y, odd, high));
+      if (p.z) o *= zv * sigmoid(zv);
+      if (slice < 4 && t + own < len) out[(long)(t + own) * D] = (TI)o;
     }
-    y = __builtin_fmaf(skip, xv, sum_lanes<LC>(y));
-    if (p.z) y *= zv * sigmoid(zv);
-    if (lane == 0) out[(long)t * D] = (TI)y;
-  }
   store_vals<float, 4>(p.hT + sat, h);
 }
 
@@ -394,65 +517,55 @@ __device__ static inline void bwd_map(const SsmParams& p, long k, int tiles, int
     P[i] = 1.f;
   }
   const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
-  const long at = s.row0 * D + d;
-  const TI* x = static_cast<const TI*>(p.x) + at;
-  const TI* dt = static_cast<const TI*>(p.dt) + at;
-  const TI* z = p.z ? static_cast<const TI*>(p.z) + at : x;
-  const TI* dout = static_cast<const TI*>(p.dout) + at;
+  uint32_t at = (uint32_t)d * sizeof(TI);
+  const TI* x = static_cast<const TI*>(p.x) + s.row0 * D;
+  const TI* dt = static_cast<const TI*>(p.dt) + s.row0 * D;
+  const TI* z = (p.z ? static_cast<const TI*>(p.z) : static_cast<const TI*>(p.x)) + s.row0 * D;
+  const TI* dout = static_cast<const TI*>(p.dout) + s.row0 * D;
   const TI* bk = static_cast<const TI*>(p.b) + (s.row0 * p.G + g) * N + part * 16;
   const TI* ck = static_cast<const TI*>(p.c) + (s.row0 * p.G + g) * N + part * 16;
   const int len = s.len;
   float S = 0.f;
-  TI xn[FLIGHT], dn[FLIGHT], zn[FLIGHT], gn[FLIGHT];
-  Keys16<TI> bn, cn;
   if (len > 0) {
+    uint32_t xn[FLIGHT], dn[FLIGHT], zn[FLIGHT], gn[FLIGHT];
+    auto load = [&](int f, int t) {
+      const long o = (long)min(t, len - 1) * D;
+      xn[f] = Row<TI>::load(x + o, at);
+      dn[f] = Row<TI>::load(dt + o, at);
+      zn[f] = Row<TI>::load(z + o, at);
+      gn[f] = Row<TI>::load(dout + o, at);
+    };
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      const long o = (long)min(f, len - 1) * D;
-      xn[f] = x[o];
-      dn[f] = dt[o];
-      zn[f] = z[o];
-      gn[f] = dout[o];
-    }
-    bn.load(bk);
-    cn.load(ck);
-  }
-  for (int t = 0; t < len; t += FLIGHT) {
-    TI xr[FLIGHT], dr[FLIGHT], zr[FLIGHT], gr[FLIGHT];
+    for (int f = 0; f < FLIGHT; ++f) load(f, f);
+    KeyPair<TI, true> keys[2];
+    keys[0].load(bk, ck);
+    // as ssm_kernel: no branch, tokens behind the last take a step of zero and
+    // have no gradient
+    for (int t = 0; t < len; t += FLIGHT)
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      xr[f] = xn[f];
-      dr[f] = dn[f];
-      zr[f] = zn[f];
-      gr[f] = gn[f];
-      const long o = (long)min(t + FLIGHT + f, len - 1) * D;
-      xn[f] = x[o];
-      dn[f] = dt[o];
-      zn[f] = z[o];
-      gn[f] = dout[o];
-    }
+      for (int f = 0; f < FLIGHT; ++f) {
+        const bool there = t + f < len;
+        const float zv = Row<TI>::widen(zn[f]), xv = Row<TI>::widen(xn[f]), gate = zv * sigmoid(zv);
+        const float step = step_of(Row<TI>::widen(dn[f]) + bias, p.softplus), st = there ? step : 0.f, u = st * xv;
+        const float dy = there ? Row<TI>::widen(gn[f]) * (p.z ? gate : 1.f) : 0.f;
+        load(f, t + FLIGHT + f);
+        S += st;
+        KeyPair<TI, true>&now = keys[f & 1], &next = keys[(f + 1) & 1];
+        const long more = t + f + 1 < len ? KS : 0;
+        bk += more;
+        ck += more;
+        now.arrive();
+        __builtin_amdgcn_sched_barrier(0);
+        next.load(bk, ck);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      if (t + f >= len) break;
-      const float st = step_of((float)dr[f] + bias, p.softplus), u = st * (float)xr[f];
-      float dy = (float)gr[f];
-      if (p.z) {
-        const float zv = (float)zr[f];
-        dy *= zv * sigmoid(zv);
+        for (int i = 0; i < 16; ++i) {
+          const float a = __builtin_amdgcn_exp2f(st * A[i]);
+          E[i] = __builtin_fmaf(a, E[i], u * now.b[i]);
+          P[i] *= a;
+          R[i] = __builtin_fmaf(P[i], dy * now.c[i], R[i]);
+        }
       }
-      S += st;
-      const Keys16<TI> bv = bn, cv = cn;
-      const long next = (long)min(t + f + 1, len - 1) * KS;
-      bn.load(bk + next);
-      cn.load(ck + next);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a = __builtin_amdgcn_exp2f(st * A[i]);
-        E[i] = __builtin_fmaf(a, E[i], u * bv[i]);
-        P[i] *= a;
-        R[i] = __builtin_fmaf(P[i], dy * cv[i], R[i]);
-      }
-    }
   }
   if (c >= p.Dg) return;
   store_states<16>(p.E + sat, E);
@@ -482,30 +595,6 @@ __global__ __launch_bounds__(256) void ssm_bwd_maps_kernel(const SsmParams p) {
 
 constexpr int BT = 8, NB = 4, BL = BT * NB;
 
-template <int J>
-__device__ static inline float from_quad(float x) {
-  return dpp<J * 0x55>(x);
-}
-
-__device__ static inline Vals<4> quad(float x) {
-  return {{from_quad<0>(x), from_quad<1>(x), from_quad<2>(x), from_quad<3>(x)}};
-}
-
-// Four sums over a quad's lanes, one for each of its channels: lane j gets the
-// j-th, and with more than four lanes a channel, the sum over all of them.
-template <int LC>
-__device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
-  const float a = (odd ? v[1] : v[0]) + dpp<0xB1>(odd ? v[0] : v[1]);
-  const float b = (odd ? v[3] : v[2]) + dpp<0xB1>(odd ? v[2] : v[3]);
-  float r = (high ? b : a) + dpp<0x4E>(high ? a : b);
-  if constexpr (LC == 8) r += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(r), (4 << 10) | 0x1f));
-  if constexpr (LC == 16) {
-    r += dpp<0x128>(r);  // row_ror 8
-    r += dpp<0x124>(r);  // row_ror 4
-  }
-  return r;
-}
-
 // a and b become (a's lanes below 32, b's below 32) and (a's from 32 on, b's
 // from 32 on): their sum then holds a's over both halves in the lower lanes
 // and b's in the upper ones, one instruction and one addition for two sums.
@@ -521,13 +610,12 @@ __device__ static inline void swap_rows(float& a, float& b) {
   b = __uint_as_float(r[1]);
 }
 
-template <typename TI, int N>
-__global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
+template <typename TI, int N, bool GATE>
+__global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(const SsmParams p) {
   constexpr int LC = N / 4;            // lanes a channel
   constexpr int CT = 1024 / N;         // channels a wave
   __shared__ __attribute__((aligned(16))) float key[BL][2][N];
   __shared__ __attribute__((aligned(16))) float start[4][NB - 2][16][64];
-  __shared__ float steps[4][BL][64];
   __shared__ __attribute__((aligned(16))) float part[2][4][BT][2][N];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -545,14 +633,16 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
   // gradients of zero, so that they add nothing to the sums over channels.
   const bool real = cown < p.Dg, mine = real && slice < 4;
   const int own = g * p.Dg + min(cown, p.Dg - 1);
-  int ch[4];
+  // places in a row of channels (bytes) and in a segment's states (floats)
+  uint32_t lane_at = (uint32_t)own * sizeof(TI), state_at[4];
+  const uint32_t mine_at = mine ? lane_at : ~0u;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) ch[c] = g * p.Dg + min(c0 + c, p.Dg - 1);
+  for (int c = 0; c < 4; ++c) state_at[c] = (uint32_t)(g * p.Dg + min(c0 + c, p.Dg - 1)) * N + slice * 4;
 
   float A[4][4], dA[4][4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const Vals<4> a = load_vals<float, 4>(p.A_log + (long)ch[c] * N + slice * 4);
+    const Vals<4> a = load_vals<float, 4>(p.A_log + state_at[c]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       A[c][j] = -LOG2E * expf(a[j]);
@@ -588,8 +678,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
     float h[4][4], l[4][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const long o = (slot * D + ch[c]) * N + slice * 4;
-      const Vals<4> e = load_vals<float, 4>(p.E + o), q = load_vals<float, 4>(p.R + o);
+      const Vals<4> e = load_vals<float, 4>(p.E + slot * D * N + state_at[c]);
+      const Vals<4> q = load_vals<float, 4>(p.R + slot * D * N + state_at[c]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         h[c][j] = e[j];
@@ -597,25 +687,31 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
       }
     }
     const int blocks = (len + BT - 1) / BT;
-    // steps of all tokens; the states at the blocks' starts
+    // the states at the blocks' starts
+    const long at = row0 * D;
 #pragma unroll 1
-    for (int t = 0; t < blocks * BT; ++t) {
-      const long o = (row0 + min(t, len - 1)) * D + own;
-      const float st = t < len ? step_of((float)dts[o] + bias, p.softplus) : 0.f;
-      steps[wave][t][lane] = st;
-      if (t >= (blocks - 1) * BT) continue;
-      const Vals<4> sv = quad(st), uv = quad(st * (float)xs[o]);
-      const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]);
+    for (int blk = 0; blk < blocks - 1; ++blk) {
+      uint32_t xr[BT], dr[BT];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[c][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[c] * A[c][j]), h[c][j], uv[c] * b[j]);
-      if ((t + 1) % BT == 0 && t + 1 < (blocks - 1) * BT) {
-        const int m = (t + 1) / BT - 1;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) start[wave][m][e][lane] = h[e >> 2][e & 3];
+      for (int i = 0; i < BT; ++i) {
+        const long o = at + (long)(blk * BT + i) * D;
+        xr[i] = Row<TI>::load(xs + o, lane_at);
+        dr[i] = Row<TI>::load(dts + o, lane_at);
       }
+#pragma unroll
+      for (int i = 0; i < BT; ++i) {
+        const float st = step_of(Row<TI>::widen(dr[i]) + bias, p.softplus);
+        const Vals<4> sv = quad(st), uv = quad(st * Row<TI>::widen(xr[i]));
+        const Vals<4> b = load_vals<float, 4>(&key[blk * BT + i][0][slice * 4]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[c][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[c] * A[c][j]), h[c][j], uv[c] * b[j]);
+      }
+      if (blk + 1 < blocks - 1)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) start[wave][blk][e][lane] = h[e >> 2][e & 3];
     }
 
 #pragma unroll 1
@@ -628,25 +724,36 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const Vals<4> e = load_vals<float, 4>(p.E + (slot * D + ch[c]) * N + slice * 4);
+            const Vals<4> e = load_vals<float, 4>(p.E + slot * D * N + state_at[c]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[c][j] = e[j];
           }
         }
       }
       // forwards: the states before each token; outputs for the gate's gradient
-      float before[BT][4][4], xo[BT], dyo[BT];
+      float before[BT][4][4], dyo[BT], sto[BT];
+      uint32_t xr[BT], dr[BT], gr[BT], zr[BT];
 #pragma unroll
       for (int i = 0; i < BT; ++i) {
-        const int t = t0 + i;
-        const bool there = i < cnt;
-        const long o = (row0 + min(t, len - 1)) * D + own;
-        const float x = there && real ? (float)xs[o] : 0.f;
-        float dy = there && real ? (float)gs[o] : 0.f;
-        const float st = steps[wave][t][lane];
-        xo[i] = x;
+        const long o = at + (long)min(t0 + i, len - 1) * D;
+        xr[i] = Row<TI>::load(xs + o, lane_at);
+        dr[i] = Row<TI>::load(dts + o, lane_at);
+        gr[i] = Row<TI>::load(gs + o, lane_at);
+        if (GATE) zr[i] = Row<TI>::load(zs + o, lane_at);
+      }
+#pragma unroll
+      for (int i = 0; i < BT; ++i) {
+        // token by token: what the compiler would load ahead, it has no registers for
+        __builtin_amdgcn_sched_barrier(0);
+        const int t = min(t0 + i, len - 1);
+        const bool there = i < cnt && real;
+        xr[i] = there ? xr[i] : 0;
+        const float x = Row<TI>::widen(xr[i]), z = GATE ? Row<TI>::widen(zr[i]) : 0.f, q = sigmoid(z);
+        const float step = step_of(Row<TI>::widen(dr[i]) + bias, p.softplus), st = i < cnt ? step : 0.f;
+        float dy = there ? Row<TI>::widen(gr[i]) : 0.f;
+        sto[i] = st;
         const Vals<4> sv = quad(st), uv = quad(st * x);
-        const Vals<4> b = load_vals<float, 4>(&key[min(t, len - 1)][0][slice * 4]);
+        const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -654,86 +761,88 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
             before[i][c][j] = h[c][j];
             h[c][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[c] * A[c][j]), h[c][j], uv[c] * b[j]);
           }
-        if (p.z) {
-          const float z = (float)zs[o], q = sigmoid(z);
-          if (p.dz) {
-            const Vals<4> c4 = load_vals<float, 4>(&key[min(t, len - 1)][1][slice * 4]);
-            Vals<4> y;
+        if constexpr (GATE) {
+          const Vals<4> c4 = load_vals<float, 4>(&key[t][1][slice * 4]);
+          Vals<4> y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              y[c] = 0.f;
+          for (int c = 0; c < 4; ++c) {
+            y[c] = 0.f;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) y[c] = __builtin_fmaf(c4[j], h[c][j], y[c]);
-            }
-            const float yo = __builtin_fmaf(skip, x, sum_own<LC>(y, odd, high));
-            if (mine && there)
-              static_cast<TI*>(p.dz)[o] = (TI)(dy * yo * (q * __builtin_fmaf(z, 1.f - q, 1.f)));
+            for (int j = 0; j < 4; ++j) y[c] = __builtin_fmaf(c4[j], h[c][j], y[c]);
           }
-          dy *= z * q;
+          const float yo = __builtin_fmaf(skip, x, sum_own<LC>(y, odd, high));
+          Row<TI>::store_inside(static_cast<TI*>(p.dz) + at + (long)t * D, i < cnt && p.dz ? D * (int)sizeof(TI) : 0, mine_at,
+                                dy * yo * (q * __builtin_fmaf(z, 1.f - q, 1.f)));
         }
-        dyo[i] = dy;
+        dyo[i] = GATE ? dy * z * q : dy;
       }
-      // backwards
+      // Backwards.  The empty assembly hides that a token's keys, steps and decays
+      // are those of above: kept since then, they would take 36 registers a token.
+      // No branch within: it would draw sums behind it, and their terms with them.
 #pragma unroll
       for (int i = BT - 1; i >= 0; --i) {
-        const int t = t0 + i;
-        if (i < cnt) {
-          const float st = steps[wave][t][lane];
-          const Vals<4> sv = quad(st), uv = quad(st * xo[i]), gv = quad(dyo[i]);
-          const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]), cc = load_vals<float, 4>(&key[t][1][slice * 4]);
-          Vals<4> lb, mA, db, dc;
+        __builtin_amdgcn_sched_barrier(0);
+        // (tokens behind the last: a step and gradients of zero, nothing stored)
+        int t = min(t0 + i, len - 1);
+        asm("" : "+s"(t));
+        const int bytes = i < cnt ? D * (int)sizeof(TI) : 0;
+        const float xo = Row<TI>::widen(xr[i]);
+        float st = sto[i];
+        asm("" : "+v"(st));
+        const Vals<4> sv = quad(st), uv = quad(st * xo), gv = quad(dyo[i]);
+        const Vals<4> b = load_vals<float, 4>(&key[t][0][slice * 4]), cc = load_vals<float, 4>(&key[t][1][slice * 4]);
+        Vals<4> lb, mA, db, dc;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) lb[c] = mA[c] = db[c] = dc[c] = 0.f;
+        for (int c = 0; c < 4; ++c) lb[c] = mA[c] = db[c] = dc[c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float now = i == BT - 1 ? h[c][j] : before[i + 1 < BT ? i + 1 : i][c][j];
-              const float lv = __builtin_fmaf(cc[j], gv[c], l[c][j]);
-              db[j] = __builtin_fmaf(lv, uv[c], db[j]);
-              lb[c] = __builtin_fmaf(lv, b[j], lb[c]);
-              dc[j] = __builtin_fmaf(now, gv[c], dc[j]);
-              l[c][j] = lv * __builtin_amdgcn_exp2f(sv[c] * A[c][j]);
-              const float m = l[c][j] * before[i][c][j];
-              mA[c] = __builtin_fmaf(m, A[c][j], mA[c]);
-              dA[c][j] = __builtin_fmaf(m, sv[c], dA[c][j]);
-            }
-          const float lbo = sum_own<LC>(lb, odd, high), mAo = sum_own<LC>(mA, odd, high);
-          const long o = (row0 + t) * D + own;
-          // A is held times log2(e)
-          float ds = __builtin_fmaf(xo[i], lbo, mAo * 0.693147181f);
-          if (p.softplus) ds *= sigmoid((float)dts[o] + bias);
-          const float dx = __builtin_fmaf(st, lbo, skip * dyo[i]);
-          if (mine) {
-            static_cast<TI*>(p.dx)[o] = (TI)dx;
-            static_cast<TI*>(p.ddt)[o] = (TI)ds;
-            dD = __builtin_fmaf(dyo[i], xo[i], dD);
-            dbias += ds;
-          }
-          // the sums over the channels' lanes, LC apart
-          swap_halves(db[0], db[2]);
-          swap_halves(db[1], db[3]);
-          swap_halves(dc[0], dc[2]);
-          swap_halves(dc[1], dc[3]);
-          float d0 = db[0] + db[2], d1 = db[1] + db[3], e0 = dc[0] + dc[2], e1 = dc[1] + dc[3];
-          swap_rows(d0, d1);
-          swap_rows(e0, e1);
-          float sd = d0 + d1, se = e0 + e1;
-          // lanes 0..15 hold state 0 of the slice, 16..31 state 1, 32..47 state 2, 48..63 state 3
-          if constexpr (LC <= 8) {
-            sd += dpp<0x128>(sd);
-            se += dpp<0x128>(se);
-          }
-          if constexpr (LC == 4) {
-            sd += dpp<0x124>(sd);
-            se += dpp<0x124>(se);
-          }
-          if ((lane & 15) < LC) {
-            const int n = slice * 4 + (lane >> 4);
-            part[turn][wave][i][0][n] = sd;
-            part[turn][wave][i][1][n] = se;
+          for (int j = 0; j < 4; ++j) {
+            const float now = i == BT - 1 ? h[c][j] : before[i + 1 < BT ? i + 1 : i][c][j];
+            const float lv = __builtin_fmaf(cc[j], gv[c], l[c][j]);
+            db[j] = __builtin_fmaf(lv, uv[c], db[j]);
+            lb[c] = __builtin_fmaf(lv, b[j], lb[c]);
+            dc[j] = __builtin_fmaf(now, gv[c], dc[j]);
+            l[c][j] = lv * __builtin_amdgcn_exp2f(sv[c] * A[c][j]);
+            const float m = l[c][j] * before[i][c][j];
+            mA[c] = __builtin_fmaf(m, A[c][j], mA[c]);
+            dA[c][j] = __builtin_fmaf(m, sv[c], dA[c][j]);
+            asm volatile("" : "+v"(dA[c][j]));  // or these sums would be formed behind the loop, of kept terms
           }
         }
+        const float lbo = sum_own<LC>(lb, odd, high), mAo = sum_own<LC>(mA, odd, high);
+        const long o = at + (long)t * D;
+        // A is held times log2(e)
+        float ds = __builtin_fmaf(xo, lbo, mAo * 0.693147181f);
+        const float slope = sigmoid(Row<TI>::widen(dr[i]) + bias);
+        ds *= p.softplus ? slope : 1.f;
+        const float dx = __builtin_fmaf(st, lbo, skip * dyo[i]);
+        Row<TI>::store_inside(static_cast<TI*>(p.dx) + o, bytes, mine_at, dx);
+        Row<TI>::store_inside(static_cast<TI*>(p.ddt) + o, bytes, mine_at, ds);
+        dD = __builtin_fmaf(dyo[i], xo, dD);
+        dbias += i < cnt ? ds : 0.f;
+        // the sums over the channels' lanes, LC apart
+        swap_halves(db[0], db[2]);
+        swap_halves(db[1], db[3]);
+        swap_halves(dc[0], dc[2]);
+        swap_halves(dc[1], dc[3]);
+        float d0 = db[0] + db[2], d1 = db[1] + db[3], e0 = dc[0] + dc[2], e1 = dc[1] + dc[3];
+        swap_rows(d0, d1);
+        swap_rows(e0, e1);
+        float sd = d0 + d1, se = e0 + e1;
+        // lanes 0..15 hold state 0 of the slice, 16..31 state 1, 32..47 state 2, 48..63 state 3
+        if constexpr (LC <= 8) {
+          sd += dpp<0x128>(sd);
+          se += dpp<0x128>(se);
+        }
+        if constexpr (LC == 4) {
+          sd += dpp<0x124>(sd);
+          se += dpp<0x124>(se);
+        }
+        // (lanes of the same state hold the same bits)
+        part[turn][wave][i][0][slice * 4 + (lane >> 4)] = sd;
+        part[turn][wave][i][1][slice * 4 + (lane >> 4)] = se;
       }
       __syncthreads();
       for (int e = tid; e < cnt * 2 * N; e += 256) {
@@ -753,7 +862,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(const SsmParams p) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (c0 + c < p.Dg)
-      store_vals<float, 4>(sums + (long)ch[c] * N + slice * 4, Vals<4>{{dA[c][0], dA[c][1], dA[c][2], dA[c][3]}});
+      store_vals<float, 4>(sums + state_at[c], Vals<4>{{dA[c][0], dA[c][1], dA[c][2], dA[c][3]}});
   if (mine) {
     sums[(long)D * N + own] = dD;
     sums[(long)D * (N + 1) + own] = dbias;
@@ -799,6 +908,9 @@ __global__ __launch_bounds__(1024) void ssm_sums_kernel(const SsmParams p) {
 
 // ------------------------------------------------------------------- host --
 
+// a grid holds fewer than 2^32 threads; the launches that may need more loop
+constexpr long long MOST_WGS = (1LL << 24) - 1;
+
 inline long long up16(long long x) { return (x + 15) & ~15LL; }
 
 int tiles_of(int Dg, int channels) { return (Dg + channels - 1) / channels; }
@@ -820,21 +932,28 @@ struct Cut {
   bool cut() const { return segments > 0; }
 };
 
-// Waves that keep the device busy: four on each of its 1,024 vector units.
+// Waves that keep the device's 1,024 vector units busy, four on each: no more,
+// or some units get a fifth and the others wait for it.
 constexpr long long WAVES = 4096;
 
-Cut cut_of(int B, int T, int D, int G, bool packed) {
+Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   Cut c = {false, std::max(T, 1), 1, 0};
   if (B == 0) return c;
   const long long tiles = (long long)G * tiles_of(D / G, 64), chains = B * tiles;
-  if (T <= 64) {
+  // Three launches and a lane a channel against one launch and N / 4 lanes: with
+  // 256 channels the same at some 160 tokens for N 16 and 360 for N 64.
+  if (T <= 96 + 4 * N) {
     c.recurrent = true;
     return c;
   }
-  if (!packed && chains >= WAVES / 2) return c;
+  if (!packed && chains > WAVES / 3) return c;
   const long long rows = packed ? T : (long long)B * T;
-  const long long L = (rows * tiles + WAVES - 1) / WAVES;
-  c.L = (int)std::max(32LL, (L + 15) / 16 * 16);
+  // rows over the segments that there may be; of packed sequences the last
+  // segments are short
+  const long long segments = std::max(1LL, packed ? WAVES / tiles - B / 2 : WAVES / chains * B);
+  long long L = (rows + segments - 1) / segments;
+  if (!packed) L = (T + segments / B - 1) / (segments / B);
+  c.L = (int)std::max(32LL, (L + FLIGHT - 1) / FLIGHT * FLIGHT);
   if (c.L >= T) {
     c.L = T;
     return c;
@@ -882,7 +1001,7 @@ BackPlan back_plan(int B, int T, int D, int G, int N, bool packed) {
 
 template <typename TI>
 void launch_outputs(const SsmParams& p, unsigned grid, bool output, hipStream_t s) {
-  const dim3 g(grid), b(256);
+  const dim3 g(grid), b(64);
   switch (p.N) {
     case 16:
       if (output) hipLaunchKernelGGL((ssm_kernel<TI, 16, true>), g, b, 0, s, p);
@@ -898,23 +1017,42 @@ void launch_outputs(const SsmParams& p, unsigned grid, bool output, hipStream_t 
   }
 }
 
+// Few states of many segments take eight threads each (20,480 states of 200
+// segments: 16 us instead of 25); many keep the device busy with one (245,760
+// states of some 13 segments: 14 us instead of 51).
+void launch_join(const SsmParams& p, long long states, int directions, hipStream_t s) {
+  const int groups = p.segments / p.B > 64 && states < 65536 ? 8 : 1;
+  const dim3 grid((unsigned)std::min(MOST_WGS, (states * groups + 255) / 256), directions);
+  if (groups > 1) hipLaunchKernelGGL((ssm_join_kernel<8>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((ssm_join_kernel<1>), grid, dim3(256), 0, s, p);
+}
+
+// One turn of four tokens in flight, two where sequences are longer than that.
+template <typename TI, int N>
+void launch_recurrent_n(const SsmParams& p, unsigned grid, hipStream_t s) {
+  if (p.rows <= 4LL * p.B) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 2>), dim3(grid), dim3(256), 0, s, p);
+}
+
 template <typename TI>
 void launch_recurrent(const SsmParams& p, unsigned grid, hipStream_t s) {
+  if (p.N == 16) launch_recurrent_n<TI, 16>(p, grid, s);
+  else if (p.N == 32) launch_recurrent_n<TI, 32>(p, grid, s);
+  else launch_recurrent_n<TI, 64>(p, grid, s);
+}
+
+template <typename TI, bool GATE>
+void launch_bwd_n(const SsmParams& p, unsigned grid, hipStream_t s) {
   const dim3 g(grid), b(256);
-  if (p.N == 16) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 16>), g, b, 0, s, p);
-  else if (p.N == 32) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 32>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((ssm_recurrent_kernel<TI, 64>), g, b, 0, s, p);
+  if (p.N == 16) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 16, GATE>), g, b, 0, s, p);
+  else if (p.N == 32) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 32, GATE>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((ssm_bwd_kernel<TI, 64, GATE>), g, b, 0, s, p);
 }
 
 template <typename TI>
 void launch_bwd(const SsmParams& p, unsigned grid, hipStream_t s) {
-  const dim3 g(grid), b(256);
-  if (p.N == 16) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 16>), g, b, 0, s, p);
-  else if (p.N == 32) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 32>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((ssm_bwd_kernel<TI, 64>), g, b, 0, s, p);
+  p.z ? launch_bwd_n<TI, true>(p, grid, s) : launch_bwd_n<TI, false>(p, grid, s);
 }
-
-constexpr long long MOST_WGS = (1LL << 24) - 1;  // a grid holds fewer than 2^32 threads; the launches that may need more loop
 
 int forward(SsmParams p, int dtype, int flags, void* workspace, long long workspace_bytes, void* stream) {
   const bool pooled = p.slots != nullptr, packed = p.cu != nullptr;
@@ -926,7 +1064,7 @@ int forward(SsmParams p, int dtype, int flags, void* workspace, long long worksp
   if (misaligned({p.x, p.dt, p.b, p.c, p.A_log, p.Dskip, p.z, p.dt_bias, p.h0, p.out, p.hT, workspace}, 16) ||
       misaligned({p.cu, p.slots}, 4))
     return GDN_ERR_INVALID_ARG;
-  Cut cut = cut_of(p.B, p.T, p.D, p.G, packed);
+  Cut cut = cut_of(p.B, p.T, p.D, p.G, p.N, packed);
   if (pooled) cut = Cut{true, std::max(p.T, 1), 1, 0};
   const Space w = space_of(cut.segments, 0, 0, p.D, p.G, p.N, 1, false);
   const long long need = cut.cut() ? w.bytes : 0;
@@ -953,15 +1091,14 @@ int forward(SsmParams p, int dtype, int flags, void* workspace, long long worksp
   p.L = cut.L;
   p.nseg = cut.nseg;
   p.segments = cut.cut() ? cut.segments : slots_of(packed, p.B, p.T, p.L);
-  const long long wgs = p.segments * p.G * tiles_of(tiles_of(p.Dg, 64), 4);
-  const long long joins = std::min(MOST_WGS, ((long long)p.B * p.D * p.N + 255) / 256);
-  if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
+  const long long wgs = p.segments * p.G * tiles_of(p.Dg, 64);
+  if (wgs > 4 * MOST_WGS) return GDN_ERR_INVALID_ARG;  // of 64 threads
   if (cut.cut()) {
     char* base = static_cast<char*>(workspace);
     p.E = reinterpret_cast<float*>(base + w.E);
     p.S = reinterpret_cast<float*>(base + w.S);
     bf ? launch_outputs<__bf16>(p, (unsigned)wgs, false, s) : launch_outputs<float>(p, (unsigned)wgs, false, s);
-    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)joins), dim3(256), 0, s, p);
+    launch_join(p, (long long)p.B * p.D * p.N, 1, s);
   }
   bf ? launch_outputs<__bf16>(p, (unsigned)wgs, true, s) : launch_outputs<float>(p, (unsigned)wgs, true, s);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -973,7 +1110,7 @@ extern "C" long long gdn_ssm_workspace_size(int B, int T, int D, int G, int N, i
   const int rc = sizes_checked(B, T, D, G, N, packed != 0, dtype);
   if (rc != GDN_OK) return rc;
   if (!backward) {
-    const Cut c = cut_of(B, T, D, G, packed != 0);
+    const Cut c = cut_of(B, T, D, G, N, packed != 0);
     return c.cut() ? space_of(c.segments, 0, 0, D, G, N, 1, false).bytes : 0;
   }
   const BackPlan b = back_plan(B, T, D, G, N, packed != 0);
@@ -1050,13 +1187,13 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = dtype == GDN_BF16;
   const long long maps = std::min(MOST_WGS, (plan.segments * G * tiles_of(p.Dg, 64) * (N / 16) + 3) / 4);
-  const long long joins = std::min(MOST_WGS, ((long long)B * D * N + 255) / 256), wgs = plan.runs * G * plan.quads;
+  const long long wgs = plan.runs * G * plan.quads;
   const long long cols = (long long)D * (N + 2);
   if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
   if (plan.segments > 0) {
     if (bf) hipLaunchKernelGGL((ssm_bwd_maps_kernel<__bf16>), dim3((unsigned)maps), dim3(256), 0, s, p);
     else hipLaunchKernelGGL((ssm_bwd_maps_kernel<float>), dim3((unsigned)maps), dim3(256), 0, s, p);
-    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)joins, 2), dim3(256), 0, s, p);
+    launch_join(p, (long long)B * D * N, 2, s);
     bf ? launch_bwd<__bf16>(p, (unsigned)wgs, s) : launch_bwd<float>(p, (unsigned)wgs, s);
     if (plan.quads > 1 && plan.rows > 0) {
       const long long total = plan.rows * G * 2 * N;

@@ -54,7 +54,7 @@ extern "C" {
  *
  * Sizes: B >= 0, T >= 0, D >= 1, G >= 1 a divisor of D; N in {16, 32, 64}
  *   (GDN_ERR_UNSUPPORTED otherwise); at most 2^30 rows, D < 2^20, B < 2^24,
- *   B * D < 2^28, B * ceil(D N / 1024) < 2^24, B * G * ceil(D / (256 G)) < 2^24.
+ *   B * D < 2^28, B * ceil(D N / 1024) < 2^24, B * G * ceil(D / (64 G)) < 2^26.
  *   dtype: GDN_F32 or GDN_BF16.
  * flags: 0 or GDN_SSM_SOFTPLUS; any other bit is GDN_ERR_INVALID_ARG.
  * Pointers: x, dt, b, c and out are required when B > 0 and T > 0, A_log and

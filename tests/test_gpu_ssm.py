@@ -72,8 +72,18 @@ def test_lengths_and_states(dtype, N, T):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [16, 32, 64])
+@pytest.mark.parametrize("D,G", [(72, 1), (130, 2)])
+def test_cut_sequences(dtype, N, D, G):
+    """Longer than what runs token by token."""
+    for T in (96 + 4 * N + 1, 401):
+        assert gdn.gdn_ssm_workspace_size(1, T, D, G, N, 0, 1) > 0
+        check_forward(*make(N + T, dtype, [T], D, G, N, False), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D,G", [(1, 1), (7, 1), (64, 1), (65, 1), (130, 2), (96, 4), (12, 12), (300, 1), (520, 2)])
-@pytest.mark.parametrize("T", [9, 80])
+@pytest.mark.parametrize("T", [9, 170])
 def test_channels_and_groups(dtype, D, G, T):
     t, c = make(D + G, dtype, [T], D, G, 16 if D != 130 else 32, False)
     check_forward(t, c, dtype)
@@ -83,7 +93,7 @@ def test_channels_and_groups(dtype, D, G, T):
 @pytest.mark.parametrize("without", [("D",), ("z",), ("dt_bias",), ("h0",), ("D", "z", "dt_bias", "h0")])
 @pytest.mark.parametrize("soft", [True, False])
 def test_options(without, soft):
-    t, c = make(5, "f32", [75] * 2, 40, 2, 16, False, without)
+    t, c = make(5, "f32", [175] * 2, 40, 2, 16, False, without)
     if not soft:
         t["dt"].abs_().mul_(0.1)
         c["dt"] = f64(t["dt"]).reshape(c["x"].shape)
@@ -111,7 +121,7 @@ def test_packed_wide_states(N):
 
 def test_enough_channels_for_no_cut():
     """2,048 tiles of channels: sequences run as they are, and cut ones agree with them."""
-    T, B, D = 70, 2048, 8
+    T, B, D = 170, 2048, 8
     assert gdn.gdn_ssm_workspace_size(B, T, D, 1, 16, 0, 1) == 0
     t, c = make(1, "bf16", [T] * B, D, 1, 16, False)
     out, hT = forward(t)
@@ -240,7 +250,7 @@ def test_no_tokens():
 
 
 def test_non_finite_values_stay_with_their_channel():
-    t, _ = make(11, "f32", [90], 20, 1, 16, False)
+    t, _ = make(11, "f32", [190], 20, 1, 16, False)
     out, hT = forward(t)
     for n, bad in (("x", float("nan")), ("z", float("inf")), ("dt", float("nan"))):
         u = {**t, n: t[n].clone()}
