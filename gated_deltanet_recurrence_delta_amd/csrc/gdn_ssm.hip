@@ -490,7 +490,7 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
 
 // ---------------------------------------------------------------- backwards --
 //
-// Segments of BL tokens.  A first launch forms, for sixteen states of a
+// Segments of some 25 tokens.  A first launch forms, for sixteen states of a
 // channel, what a segment leaves from zero: the state E going forwards and,
 // going backwards in time, the state's gradient, R = sum_t exp(A (s_1 + .. +
 // s_t)) c_t dy_t, which one forward walk gives too.  The join makes of them the
@@ -593,7 +593,15 @@ __global__ __launch_bounds__(256) void ssm_bwd_maps_kernel(const SsmParams p) {
 // blocks' starts; then, from the last block on, a block's states are formed
 // again and kept in registers, and its tokens are taken backwards.
 
-constexpr int BT = 8, NB = 4, BL = BT * NB;
+// More tokens a block need more registers, more blocks more LDS (a workgroup of
+// four waves has 80 KB of it and 256 registers, so that two share a compute
+// unit), and shorter segments more joining (4 x 4,096 x 1,280, N 16, whole
+// calls: 4 x 6 505 us, 4 x 5 542, 5 x 6 522, 6 x 5 541, 8 x 4 560).
+template <int N>
+struct Blocks {
+  static constexpr int BT = 4, NB = N == 16 ? 6 : 5, BL = BT * NB;
+};
+int segment_rows(int N) { return N == 16 ? Blocks<16>::BL : N == 32 ? Blocks<32>::BL : Blocks<64>::BL; }
 
 // a and b become (a's lanes below 32, b's below 32) and (a's from 32 on, b's
 // from 32 on): their sum then holds a's over both halves in the lower lanes
@@ -610,21 +618,22 @@ __device__ static inline void swap_rows(float& a, float& b) {
   b = __uint_as_float(r[1]);
 }
 
-template <typename TI, int N, bool GATE>
-__global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(const SsmParams p) {
+template <typename TI, int N, bool GATE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmParams p) {
+  constexpr int BT = Blocks<N>::BT, NB = Blocks<N>::NB, BL = BT * NB, NT = 64 * WAVES;
   constexpr int LC = N / 4;            // lanes a channel
   constexpr int CT = 1024 / N;         // channels a wave
   __shared__ __attribute__((aligned(16))) float key[BL][2][N];
-  __shared__ __attribute__((aligned(16))) float start[4][NB - 2][16][64];
-  __shared__ __attribute__((aligned(16))) float part[2][4][BT][2][N];
+  __shared__ __attribute__((aligned(16))) float start[WAVES][NB - 2][16][64];
+  __shared__ __attribute__((aligned(16))) float part[2][WAVES][BT][2][N];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tiles = (p.Dg + CT - 1) / CT, quads = (tiles + 3) >> 2;
+  const int tiles = (p.Dg + CT - 1) / CT, teams = (tiles + WAVES - 1) / WAVES;
   int k = blockIdx.x;
-  const int tq = k % quads;
-  k /= quads;
+  const int team = k % teams;
+  k /= teams;
   const int g = k % p.G, run = k / p.G;
-  const int D = p.D, tile = tq * 4 + wave;
+  const int D = p.D, tile = team * WAVES + wave;
   const int slice = lane % LC, group = lane / LC;
   const bool odd = lane & 1, high = lane & 2;
   // channels of the lane's block, and its own
@@ -667,7 +676,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(const SsmParams p) {
     const long row0 = s.row0;
     const int len = s.len;
     __syncthreads();  // the keys of the segment before have been read
-    for (int i = tid; i < len * N; i += 256) {
+    for (int i = tid; i < len * N; i += NT) {
       const int t = i / N, n = i % N;
       const long o = ((row0 + t) * p.G + g) * N + n;
       key[t][0][n] = (float)bs[o];
@@ -845,14 +854,14 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(const SsmParams p) {
         part[turn][wave][i][1][slice * 4 + (lane >> 4)] = se;
       }
       __syncthreads();
-      for (int e = tid; e < cnt * 2 * N; e += 256) {
+      for (int e = tid; e < cnt * 2 * N; e += NT) {
         const float* q = &part[turn][0][0][0][0] + e;
         constexpr int W = BT * 2 * N;
-        const float v = (q[0] + q[W]) + (q[2 * W] + q[3 * W]);
+        const float v = WAVES == 2 ? q[0] + q[W] : (q[0] + q[W]) + (q[2 * W] + q[3 * W]);
         const int i = e / (2 * N), which = e / N % 2, n = e % N;
         const long o = ((row0 + t0 + i) * p.G + g) * N + n;
-        if (quads == 1) static_cast<TI*>(which ? p.dc : p.db)[o] = (TI)v;
-        else p.keys[(((long)tq * p.rows + row0 + t0 + i) * p.G + g) * 2 * N + which * N + n] = v;
+        if (teams == 1) static_cast<TI*>(which ? p.dc : p.db)[o] = (TI)v;
+        else p.keys[(((long)team * p.rows + row0 + t0 + i) * p.G + g) * 2 * N + which * N + n] = v;
       }
       turn ^= 1;
     }
@@ -872,14 +881,14 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(const SsmParams p) {
 // db and dc of the workgroups' sums, where a group's channels are several
 // workgroups'.  Rows of no sequence are left as they were.
 template <typename TI>
-__global__ __launch_bounds__(256) void ssm_keys_kernel(const SsmParams p, int quads) {
+__global__ __launch_bounds__(256) void ssm_keys_kernel(const SsmParams p, int teams) {
   const long GN = (long)p.G * p.N, total = p.rows * GN * 2;
   for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long)gridDim.x * 256) {
     const int n = (int)(e % p.N), which = (int)(e / p.N % 2);
     const long rg = e / (2 * p.N), row = rg / p.G;
     if (p.cu && (row < p.cu[0] || row >= p.cu[p.B])) continue;
     float a = 0.f;
-    for (int q = 0; q < quads; ++q) a += p.keys[(long)q * total + e];
+    for (int q = 0; q < teams; ++q) a += p.keys[(long)q * total + e];
     static_cast<TI*>(which ? p.dc : p.db)[rg * p.N + n] = (TI)a;
   }
 }
@@ -968,33 +977,46 @@ struct Space {
   long long E, R, S, keys, sums, bytes;
 };
 
-Space space_of(long long segments, long long runs, long long rows, int D, int G, int N, int quads, bool back) {
+Space space_of(long long segments, long long runs, long long rows, int D, int G, int N, int teams, bool back) {
   Space w = {};
   const long long state = up16(segments * D * N * 4);
   w.E = 0;
   w.R = w.E + state;
   w.S = w.R + (back ? state : 0);
   w.keys = w.S + up16(segments * D * 4);
-  w.sums = w.keys + (back && quads > 1 ? up16(rows * G * 2 * N * 4 * quads) : 0);
+  w.sums = w.keys + (back && teams > 1 ? up16(rows * G * 2 * N * 4 * teams) : 0);
   w.bytes = w.sums + (back ? up16(runs * D * (N + 2) * 4) : 0);
   return w;
 }
 
 struct BackPlan {
   long long segments, runs, rows;
-  int nseg, run, quads;
+  int nseg, run, waves, teams;
 };
 
 BackPlan back_plan(int B, int T, int D, int G, int N, bool packed) {
   BackPlan b;
   b.rows = (packed ? 1LL : B) * (long long)T;
-  b.nseg = segments_of(T, BL);
-  b.segments = B > 0 ? slots_of(packed, B, T, BL) : 0;
-  b.quads = tiles_of(tiles_of(D / G, 1024 / N), 4);
-  // Workgroups in two rounds or more on 512 places (two a compute unit), each
-  // with as many segments as that leaves: few partial sums.
-  const long long wide = (long long)b.quads * G;
-  b.run = (int)std::max(1LL, b.segments * wide / 1024);
+  const int L = segment_rows(N), tiles = tiles_of(D / G, 1024 / N);
+  b.nseg = segments_of(T, L);
+  b.segments = B > 0 ? slots_of(packed, B, T, L) : 0;
+  // Four waves a workgroup, or two where the last one of a group's would
+  // otherwise have two to work for nothing.
+  b.waves = (tiles + 3) / 4 * 4 - tiles >= 2 ? 2 : 4;
+  b.teams = tiles_of(tiles, b.waves);
+  // A workgroup takes a run of segments (few partial sums of the parameters'
+  // gradients), as long as the device's places (eight waves a compute unit)
+  // are in the end filled as well as by shorter ones.
+  const long long wide = (long long)b.teams * G, places = 2048 / b.waves;
+  const int first = (int)std::max(1LL, b.segments * wide / (8 * places));
+  long long best = 0;
+  for (int run = first; run < first + 64; ++run) {
+    // (a workgroup's beginning and end take about half a segment's time)
+    const long long rounds = ((b.segments + run - 1) / run * wide + places - 1) / places * (2 * run + 1);
+    if (run > first && rounds > best) continue;
+    best = rounds;
+    b.run = run;
+  }
   b.runs = (b.segments + b.run - 1) / b.run;
   return b;
 }
@@ -1041,17 +1063,18 @@ void launch_recurrent(const SsmParams& p, unsigned grid, hipStream_t s) {
   else launch_recurrent_n<TI, 64>(p, grid, s);
 }
 
-template <typename TI, bool GATE>
+template <typename TI, bool GATE, int WAVES>
 void launch_bwd_n(const SsmParams& p, unsigned grid, hipStream_t s) {
-  const dim3 g(grid), b(256);
-  if (p.N == 16) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 16, GATE>), g, b, 0, s, p);
-  else if (p.N == 32) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 32, GATE>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((ssm_bwd_kernel<TI, 64, GATE>), g, b, 0, s, p);
+  const dim3 g(grid), b(64 * WAVES);
+  if (p.N == 16) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 16, GATE, WAVES>), g, b, 0, s, p);
+  else if (p.N == 32) hipLaunchKernelGGL((ssm_bwd_kernel<TI, 32, GATE, WAVES>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((ssm_bwd_kernel<TI, 64, GATE, WAVES>), g, b, 0, s, p);
 }
 
 template <typename TI>
-void launch_bwd(const SsmParams& p, unsigned grid, hipStream_t s) {
-  p.z ? launch_bwd_n<TI, true>(p, grid, s) : launch_bwd_n<TI, false>(p, grid, s);
+void launch_bwd(const SsmParams& p, int waves, unsigned grid, hipStream_t s) {
+  if (waves == 2) p.z ? launch_bwd_n<TI, true, 2>(p, grid, s) : launch_bwd_n<TI, false, 2>(p, grid, s);
+  else p.z ? launch_bwd_n<TI, true, 4>(p, grid, s) : launch_bwd_n<TI, false, 4>(p, grid, s);
 }
 
 int forward(SsmParams p, int dtype, int flags, void* workspace, long long workspace_bytes, void* stream) {
@@ -1114,7 +1137,7 @@ extern "C" long long gdn_ssm_workspace_size(int B, int T, int D, int G, int N, i
     return c.cut() ? space_of(c.segments, 0, 0, D, G, N, 1, false).bytes : 0;
   }
   const BackPlan b = back_plan(B, T, D, G, N, packed != 0);
-  return space_of(b.segments, b.runs, b.rows, D, G, N, b.quads, true).bytes;
+  return space_of(b.segments, b.runs, b.rows, D, G, N, b.teams, true).bytes;
 }
 
 extern "C" int gdn_ssm_fwd(const void* x, const void* dt, const void* b, const void* c, const float* A_log,
@@ -1157,7 +1180,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
                   workspace}, 16) || misaligned(cu_seqlens, 4))
     return GDN_ERR_INVALID_ARG;
   const BackPlan plan = back_plan(B, T, D, G, N, packed);
-  const Space w = space_of(plan.segments, plan.runs, plan.rows, D, G, N, plan.quads, true);
+  const Space w = space_of(plan.segments, plan.runs, plan.rows, D, G, N, plan.teams, true);
   if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return GDN_ERR_INVALID_ARG;
   const long long e = dtype == GDN_BF16 ? 2 : 4, data = plan.rows * D * e, keys = plan.rows * G * N * e;
   const long long state = (long long)B * D * N * 4, rates = 4LL * D * N, vec = 4LL * D;
@@ -1177,7 +1200,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
   p.keys = reinterpret_cast<float*>(base + w.keys);
   p.sums = reinterpret_cast<float*>(base + w.sums);
   p.B = B; p.T = T; p.D = D; p.G = G; p.N = N; p.Dg = D / G;
-  p.L = BL;
+  p.L = segment_rows(N);
   p.nseg = plan.nseg;
   p.segments = plan.segments;
   p.run = plan.run;
@@ -1187,19 +1210,19 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = dtype == GDN_BF16;
   const long long maps = std::min(MOST_WGS, (plan.segments * G * tiles_of(p.Dg, 64) * (N / 16) + 3) / 4);
-  const long long wgs = plan.runs * G * plan.quads;
+  const long long wgs = plan.runs * G * plan.teams;
   const long long cols = (long long)D * (N + 2);
   if (wgs > MOST_WGS) return GDN_ERR_INVALID_ARG;
   if (plan.segments > 0) {
     if (bf) hipLaunchKernelGGL((ssm_bwd_maps_kernel<__bf16>), dim3((unsigned)maps), dim3(256), 0, s, p);
     else hipLaunchKernelGGL((ssm_bwd_maps_kernel<float>), dim3((unsigned)maps), dim3(256), 0, s, p);
     launch_join(p, (long long)B * D * N, 2, s);
-    bf ? launch_bwd<__bf16>(p, (unsigned)wgs, s) : launch_bwd<float>(p, (unsigned)wgs, s);
-    if (plan.quads > 1 && plan.rows > 0) {
+    bf ? launch_bwd<__bf16>(p, plan.waves, (unsigned)wgs, s) : launch_bwd<float>(p, plan.waves, (unsigned)wgs, s);
+    if (plan.teams > 1 && plan.rows > 0) {
       const long long total = plan.rows * G * 2 * N;
       const unsigned grid = (unsigned)std::min<long long>(4096, (total + 255) / 256);
-      if (bf) hipLaunchKernelGGL((ssm_keys_kernel<__bf16>), dim3(grid), dim3(256), 0, s, p, plan.quads);
-      else hipLaunchKernelGGL((ssm_keys_kernel<float>), dim3(grid), dim3(256), 0, s, p, plan.quads);
+      if (bf) hipLaunchKernelGGL((ssm_keys_kernel<__bf16>), dim3(grid), dim3(256), 0, s, p, plan.teams);
+      else hipLaunchKernelGGL((ssm_keys_kernel<float>), dim3(grid), dim3(256), 0, s, p, plan.teams);
     }
   }
   hipLaunchKernelGGL(ssm_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, p);
