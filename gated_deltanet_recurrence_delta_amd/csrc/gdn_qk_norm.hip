@@ -116,13 +116,14 @@ __device__ static inline typename Raw<TS, 8>::type partners(const NormParams& p,
   return q;
 }
 
-// Rows of one token in flight at once.
-constexpr int FLIGHT = 4;
-
 template <typename TI, int D, int PAIRS, bool BACK>
 __global__ __launch_bounds__(NT) void norm_kernel(const NormParams p) {
   constexpr int LR = D / 8;  // lanes a row
   constexpr int GROUPS = NT / LR;
+  // Rows of one token in flight at once; backwards, with three vectors a row, two
+  // leave more waves (4 x 4,096 tokens, 16 + 4 heads of 128, neighbours paired:
+  // 61 us a call, 67 with four).
+  constexpr int FLIGHT = BACK ? 2 : 4;
   const int side = (int)blockIdx.x < p.wgs[0] ? 0 : 1;
   const int wg = blockIdx.x - (side ? p.wgs[0] : 0), nwg = p.wgs[side];
   const int tid = threadIdx.x, c0 = tid % LR * 8, group = tid / LR;
@@ -229,25 +230,22 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormParams p) {
   }
 }
 
-// The partial sums' sums, one workgroup for queries and one for keys: a thread
-// adds every (NT / D)-th row, then the threads of a channel are added.
-template <int D>
-__global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, float* dwq, float* dwk) {
-  constexpr int S = 1024 / D;
-  __shared__ float sums[S][D];
-  float* out = blockIdx.x ? dwk : dwq;
+// The partial sums' sums: 32 channels of one side a workgroup, 32 threads each
+// (one workgroup a side took 14 us for 2,048 rows of 128; these X).
+__global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, int d, float* dwq, float* dwk) {
+  __shared__ float sums[32][32];
+  const int side = blockIdx.y, c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  float* out = side ? dwk : dwq;
   if (!out) return;
-  const float* part = p.part[blockIdx.x];
-  const int rows = p.wgs[blockIdx.x], c = threadIdx.x % D, s = threadIdx.x / D;
+  const float* part = p.part[side] + blockIdx.x * 32 + c;
   float a = 0.f;
 #pragma unroll 8
-  for (int i = s; i < rows; i += S) a += part[(long)i * D + c];
-  sums[s][c] = a;
+  for (int i = k; i < p.wgs[side]; i += 32) a += part[(long)i * d];
+  sums[k][c] = a;
   __syncthreads();
-  if (s == 0) {
-    for (int i = 1; i < S; ++i) a += sums[i][c];
-    out[c] = a;
-  }
+  if (k) return;
+  for (int i = 1; i < 32; ++i) a += sums[i][c];
+  out[blockIdx.x * 32 + c] = a;
 }
 
 // ------------------------------------------------------------------- host --
@@ -351,14 +349,8 @@ int norm(const void* const x[2], const float* cos, const float* sin, const int32
   p.scale = flags & GDN_NORM_L2 ? 1.f : 1.f / (float)d;
   const int pairs = rot == 0 ? NONE : flags & GDN_NORM_INTERLEAVED ? NEIGHBOURS : rot % 16 ? HALVES_ODD : HALVES;
   if (tokens > 0) back ? launch<true>(p, d, pairs, dtype, s) : launch<false>(p, d, pairs, dtype, s);
-  if (weights) {
-    switch (d) {
-      case 32: hipLaunchKernelGGL((norm_weights_kernel<32>), dim3(2), dim3(1024), 0, s, p, dw[0], dw[1]); break;
-      case 64: hipLaunchKernelGGL((norm_weights_kernel<64>), dim3(2), dim3(1024), 0, s, p, dw[0], dw[1]); break;
-      case 128: hipLaunchKernelGGL((norm_weights_kernel<128>), dim3(2), dim3(1024), 0, s, p, dw[0], dw[1]); break;
-      default: hipLaunchKernelGGL((norm_weights_kernel<256>), dim3(2), dim3(1024), 0, s, p, dw[0], dw[1]); break;
-    }
-  }
+  if (weights)
+    hipLaunchKernelGGL(norm_weights_kernel, dim3(d / 32, 2), dim3(1024), 0, s, p, d, dw[0], dw[1]);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

@@ -86,11 +86,9 @@ def _placed(dev, tensors):
     if dev.type != "cuda":
         raise ValueError("all tensors must be on the same GPU device")
     for t in tensors:
-        if t is not None:
-            if t.device != dev:
-                raise ValueError("all tensors must be on the same GPU device")
-            if not t.is_contiguous():
-                raise ValueError("all tensors must be contiguous")
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError("all tensors must be on the same GPU device" if t.device != dev else
+                             "all tensors must be contiguous")
 
 
 def _like(name, t, shape, dtype):
