@@ -602,5 +602,5 @@ from .conv import (causal_conv, conv_bwd, conv_fwd, conv_fwd_pool, gdn_conv_bwd,
                    gdn_conv_fwd_pool, gdn_conv_workspace_size)
 from .ssm import (gdn_ssm_bwd, gdn_ssm_fwd, gdn_ssm_fwd_recurrent_pool, gdn_ssm_workspace_size,  # noqa: E402
                   selective_scan, ssm_bwd, ssm_fwd, ssm_fwd_recurrent_pool)
-from .qk_norm import (gdn_qk_norm_bwd, gdn_qk_norm_fwd, gdn_qk_norm_workspace_size, qk_norm, qk_norm_bwd,  # noqa: E402
-                      qk_norm_fwd)
+from .norms import (gdn_qk_norm_bwd, gdn_qk_norm_fwd, gdn_qk_norm_workspace_size, qk_norm, qk_norm_bwd,  # noqa: E402
+                    qk_norm_fwd)

@@ -51,28 +51,30 @@ def _storage(name, t):
     """The dtype code of a tensor of tokens."""
     import torch
 
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return GDN_BF16
-    if t.dtype == torch.float32:
+    if dtype is torch.float32:
         return GDN_F32
-    raise TypeError(f"{name} dtype must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"{name} dtype must be float32 or bfloat16, got {dtype}")
 
 
 def _batch(name, t, cu_seqlens, dims):
     """(B, T) of a tensor of tokens with ``dims`` dimensions behind them."""
     import torch
 
+    shape = t.shape
     if cu_seqlens is None:
-        if t.dim() != dims + 2:
+        if len(shape) != dims + 2:
             raise ValueError(f"{name} must have {dims + 2} dimensions, (B, T, ...)")
-        return t.shape[0], t.shape[1]
+        return shape[0], shape[1]
     if cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be int32")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be one-dimensional, with at least one entry")
-    if t.dim() != dims + 1:
+    if len(shape) != dims + 1:
         raise ValueError(f"packed {name} must have {dims + 1} dimensions, (T, ...)")
-    return cu_seqlens.numel() - 1, t.shape[0]
+    return cu_seqlens.numel() - 1, shape[0]
 
 
 def _optional(name, t, shape, dtype):
@@ -85,11 +87,12 @@ def _sizes(x, w, bias, cu_seqlens):
 
     dtype = _storage("x", x)
     B, T = _batch("x", x, cu_seqlens, 1)
-    D = x.shape[-1]
-    if w.dim() != 2 or w.shape[0] != D or w.dtype != torch.float32:
-        raise ValueError(f"w must be float32 of shape ({D}, W), got {w.dtype} {tuple(w.shape)}")
-    _optional("bias", bias, (D,), torch.float32)
-    return dtype, B, T, D, w.shape[1]
+    D, ws = x.shape[-1], w.shape
+    if len(ws) != 2 or ws[0] != D or w.dtype != torch.float32:
+        raise ValueError(f"w must be float32 of shape ({D}, W), got {w.dtype} {tuple(ws)}")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (D,)):
+        _like("bias", bias, (D,), torch.float32)
+    return dtype, B, T, D, ws[1]
 
 
 def conv_fwd(x, w, bias=None, h0=None, cu_seqlens=None, silu=True, out=None, hT=None, stream=None):
@@ -158,12 +161,16 @@ def _backward(x, w, dout, bias, h0, cu_seqlens, dhT, silu, want_dh0, workspace, 
 
 
 def _pool_of(pool, slots, B, state, dtype):
+    """The number of a pool's slots, pool and slots checked."""
     import torch
 
-    if pool.dim() != len(state) + 1:
-        raise ValueError(f"pool must be (slots, {', '.join(map(str, state))})")
-    _like("pool", pool, (pool.shape[0], *state), dtype)
-    _like("slots", slots, (B,), torch.int32)
+    shape = pool.shape
+    if pool.dtype != dtype or shape[1:] != state or not shape:
+        raise ValueError(f"pool must be {dtype} of shape (slots, {', '.join(map(str, state))}), got {pool.dtype} "
+                         f"{tuple(shape)}")
+    if slots.dtype != torch.int32 or slots.shape != (B,):
+        _like("slots", slots, (B,), torch.int32)
+    return shape[0]
 
 
 def conv_fwd_pool(x, w, pool, slots, bias=None, cu_seqlens=None, silu=True, out=None, stream=None):
@@ -177,14 +184,15 @@ def conv_fwd_pool(x, w, pool, slots, bias=None, cu_seqlens=None, silu=True, out=
     import torch
 
     dtype, B, T, D, W = _sizes(x, w, bias, cu_seqlens)
-    _pool_of(pool, slots, B, (W - 1, D), x.dtype)
-    _optional("out", out, x.shape, x.dtype)
+    nslots = _pool_of(pool, slots, B, (W - 1, D), x.dtype)
     dev = x.device
-    _placed(dev, (x, w, bias, pool, slots, cu_seqlens, out))
     if out is None:
         out = torch.empty_like(x)
+    else:
+        _like("out", out, x.shape, x.dtype)
+    _placed(dev, (x, w, bias, pool, slots, cu_seqlens, out))
     _call("gdn_conv_fwd_pool", dev, x.data_ptr(), w.data_ptr(), _ptr(bias), pool.data_ptr(), slots.data_ptr(),
-          _ptr(cu_seqlens), out.data_ptr(), pool.shape[0], B, T, D, W, _raw_stream(dev, stream), dtype,
+          _ptr(cu_seqlens), out.data_ptr(), nslots, B, T, D, W, _raw_stream(dev, stream), dtype,
           GDN_CONV_SILU if silu else 0)
     return out
 

@@ -6,7 +6,7 @@ in the package's other entry points.
 from __future__ import annotations
 
 from . import load
-from .conv import _optional, _storage
+from .conv import _storage
 from .linear import _call, _like, _placed, _ptr, _raw_stream, _scratch
 
 __all__ = ["gdn_qk_norm_fwd", "gdn_qk_norm_bwd", "gdn_qk_norm_workspace_size", "qk_norm_fwd", "qk_norm_bwd", "qk_norm"]
@@ -38,31 +38,37 @@ def _checked(q, k, cos, sin, pos, wq, wk, norm, interleaved):
     """(dtype code, sizes, table sizes, flags), the inputs checked against one another."""
     import torch
 
-    dtype = _storage("q", q)
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+    dtype, f32 = _storage("q", q), torch.float32
+    qs, ks = q.shape, k.shape
+    lead, d = qs[:-2], qs[-1] if qs else 0
+    if len(lead) not in (1, 2) or len(ks) != len(qs) or ks[:-2] != lead or ks[-1] != d:
         raise ValueError("q and k must be (B, T, heads, d), or (T, heads, d) packed, of the same tokens and width")
     if k.dtype != q.dtype:
         raise TypeError(f"q and k must share one dtype, got {q.dtype}, {k.dtype}")
     if norm not in ("rms", "l2"):
         raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
-    lead, d = q.shape[:-2], q.shape[-1]
     B, T = lead if len(lead) == 2 else (1, lead[0])
     rot = P = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
-        if cos.dim() != 2 or cos.dtype != torch.float32 or cos.shape[0] < 1 or 2 * cos.shape[1] > d:
+        shape = cos.shape
+        if len(shape) != 2 or cos.dtype != f32 or shape[0] < 1 or 2 * shape[1] > d:
             raise ValueError(f"cos must be float32 of shape (positions, at most {d // 2}), got {cos.dtype} "
-                             f"{tuple(cos.shape)}")
-        _like("sin", sin, cos.shape, torch.float32)
-        P, rot = cos.shape[0], 2 * cos.shape[1]
+                             f"{tuple(shape)}")
+        if sin.dtype != f32 or sin.shape != shape:
+            _like("sin", sin, shape, f32)
+        P, rot = shape[0], 2 * shape[1]
         if rot and pos is None and len(lead) == 1:
             raise ValueError("packed rows need their positions in pos")
-    _optional("pos", pos, lead, torch.int32)
-    _optional("wq", wq, (d,), torch.float32)
-    _optional("wk", wk, (d,), torch.float32)
+    if pos is not None and (pos.dtype != torch.int32 or pos.shape != lead):
+        _like("pos", pos, lead, torch.int32)
+    if wq is not None and (wq.dtype != f32 or wq.shape != (d,)):
+        _like("wq", wq, (d,), f32)
+    if wk is not None and (wk.dtype != f32 or wk.shape != (d,)):
+        _like("wk", wk, (d,), f32)
     flags = (GDN_NORM_L2 if norm == "l2" else 0) | (GDN_NORM_INTERLEAVED if interleaved else 0)
-    return dtype, (B, T, q.shape[-2], k.shape[-2], d), (rot, P), flags
+    return dtype, (B, T, qs[-2], ks[-2], d), (rot, P), flags
 
 
 def qk_norm_fwd(q, k, cos=None, sin=None, pos=None, wq=None, wk=None, norm="rms", eps=1e-6, interleaved=False, qo=None,
@@ -82,8 +88,10 @@ def qk_norm_fwd(q, k, cos=None, sin=None, pos=None, wq=None, wk=None, norm="rms"
     import torch
 
     dtype, sizes, table, flags = _checked(q, k, cos, sin, pos, wq, wk, norm, interleaved)
-    _optional("qo", qo, q.shape, q.dtype)
-    _optional("ko", ko, k.shape, k.dtype)
+    if qo is not None:
+        _like("qo", qo, q.shape, q.dtype)
+    if ko is not None:
+        _like("ko", ko, k.shape, k.dtype)
     dev = q.device
     _placed(dev, (q, k, cos, sin, pos, wq, wk, qo, ko))
     qo = torch.empty_like(q) if qo is None else qo

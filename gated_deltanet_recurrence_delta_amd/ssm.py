@@ -55,24 +55,35 @@ def _workspace_bytes(*sizes):
 
 
 def _sizes(x, dt, b, c, A_log, D, z, dt_bias, cu_seqlens):
-    """(dtype code, B, T, channels, groups, states), the inputs checked against one another."""
+    """(dtype code, B, T, channels, groups, states), the inputs checked against one another.
+
+    (The comparisons stand here and not in _like, which says what is wrong: a call a tensor less on the way of every
+    decoded token.)"""
     import torch
 
     dtype = _storage("x", x)
     B, T = _batch("x", x, cu_seqlens, 1)
-    _like("dt", dt, x.shape, x.dtype)
-    _optional("z", z, x.shape, x.dtype)
-    channels = x.shape[-1]
-    if b.dim() != x.dim() + 1 or b.shape[:-2] != x.shape[:-1]:
-        raise ValueError(f"b must be {tuple(x.shape[:-1])} + (G, N), got {tuple(b.shape)}")
-    G, N = b.shape[-2:]
+    xt, xs, bs, f32 = x.dtype, x.shape, b.shape, torch.float32
+    channels = xs[-1]
+    if dt.dtype != xt or dt.shape != xs:
+        _like("dt", dt, xs, xt)
+    if z is not None and (z.dtype != xt or z.shape != xs):
+        _like("z", z, xs, xt)
+    if len(bs) != len(xs) + 1 or bs[:-2] != xs[:-1]:
+        raise ValueError(f"b must be {tuple(xs[:-1])} + (G, N), got {tuple(bs)}")
+    G, N = bs[-2:]
     if G < 1 or channels % G:
         raise ValueError(f"{channels} channels do not divide into {G} groups")
-    _like("b", b, b.shape, x.dtype)
-    _like("c", c, b.shape, x.dtype)
-    _like("A_log", A_log, (channels, N), torch.float32)
-    _optional("D", D, (channels,), torch.float32)
-    _optional("dt_bias", dt_bias, (channels,), torch.float32)
+    if b.dtype != xt:
+        _like("b", b, bs, xt)
+    if c.dtype != xt or c.shape != bs:
+        _like("c", c, bs, xt)
+    if A_log.dtype != f32 or A_log.shape != (channels, N):
+        _like("A_log", A_log, (channels, N), f32)
+    if D is not None and (D.dtype != f32 or D.shape != (channels,)):
+        _like("D", D, (channels,), f32)
+    if dt_bias is not None and (dt_bias.dtype != f32 or dt_bias.shape != (channels,)):
+        _like("dt_bias", dt_bias, (channels,), f32)
     return dtype, B, T, channels, G, N
 
 
@@ -162,15 +173,16 @@ def ssm_fwd_recurrent_pool(x, dt, b, c, A_log, pool, slots, D=None, z=None, dt_b
     import torch
 
     dtype, B, T, channels, G, N = _sizes(x, dt, b, c, A_log, D, z, dt_bias, cu_seqlens)
-    _pool_of(pool, slots, B, (channels, N), torch.float32)
-    _optional("out", out, x.shape, x.dtype)
+    nslots = _pool_of(pool, slots, B, (channels, N), torch.float32)
     dev = x.device
-    _placed(dev, (x, dt, b, c, A_log, D, z, dt_bias, pool, slots, cu_seqlens, out))
     if out is None:
         out = torch.empty_like(x)
+    else:
+        _like("out", out, x.shape, x.dtype)
+    _placed(dev, (x, dt, b, c, A_log, D, z, dt_bias, pool, slots, cu_seqlens, out))
     _call("gdn_ssm_fwd_recurrent_pool", dev, x.data_ptr(), dt.data_ptr(), b.data_ptr(), c.data_ptr(), A_log.data_ptr(),
           _ptr(D), _ptr(z), _ptr(dt_bias), pool.data_ptr(), slots.data_ptr(), _ptr(cu_seqlens), out.data_ptr(),
-          pool.shape[0], B, T, channels, G, N, _raw_stream(dev, stream), dtype, GDN_SSM_SOFTPLUS if softplus else 0)
+          nslots, B, T, channels, G, N, _raw_stream(dev, stream), dtype, GDN_SSM_SOFTPLUS if softplus else 0)
     return out
 
 

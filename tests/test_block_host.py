@@ -128,7 +128,7 @@ def test_norm_sizes(call):
 
 @pytest.mark.parametrize("call,kw,names", [
     (conv, {}, "x w out hT"), (conv_pool, {}, "x w out pool slots"), (conv_bwd, {}, "x w dout dx dw workspace"),
-    (ssm, dict(T=100), "x dt b c A_log out hT workspace"), (ssm_pool, {}, "x dt b c A_log out pool slots"),
+    (ssm, dict(T=400), "x dt b c A_log out hT workspace"), (ssm_pool, {}, "x dt b c A_log out pool slots"),
     (ssm_bwd, {}, "x dt b c A_log dout dx ddt db dc dA_log workspace"), (norm, dict(T=8), "q k qo ko"),
     (norm_bwd, dict(T=8), "q k dqo dko dq dk workspace")])
 def test_missing_and_misaligned_pointers(call, kw, names):
