@@ -1,8 +1,8 @@
 // Depthwise causal convolution over W tokens with SiLU, forwards, backwards
 // and on states in a pool, for gfx950.
 //
-// A lane owns V neighbouring channels (16 bytes of them where D allows) and
-// walks down a segment of its sequence with the last W - 1 tokens in
+// A lane owns V channels -- neighbours, 16 bytes of them, where D allows, else
+// 64 apart, so that a wave's loads are whole lines at any alignment -- and walks down a segment of its sequence with the last W - 1 tokens in
 // registers, so that a token is read once and, at a segment's start, W - 1 of
 // them a second time.  Bound by memory: x in, out out.
 //
@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_checks.h"
 #include "gdn_conv.h"
@@ -45,22 +46,87 @@ struct ConvParams {
   int silu;
 };
 
+// A lane's V channels and its access to rows.  NEXT: neighbours, read and
+// written at once; else 64 apart, the last tile's lanes behind D reading
+// channel D - 1 and writing nothing.
+template <typename TI, int V, bool NEXT>
+struct Channels {
+  int first, D;
+  uint32_t place[NEXT ? 1 : V];  // in a row, bytes
+  typedef typename std::conditional<NEXT, typename Raw<TI, V>::type, Vals<V>>::type raw;
+  __device__ Channels(int tile, int lane, int D_) : first(tile * 64 * V + (NEXT ? lane * V : lane)), D(D_) {
+    if constexpr (NEXT) place[0] = (uint32_t)first * sizeof(TI);
+    else
+#pragma unroll
+      for (int i = 0; i < V; ++i) place[i] = (uint32_t)min(at(i), D - 1) * sizeof(TI);
+  }
+  __device__ int at(int i) const { return NEXT ? first + i : first + 64 * i; }
+  __device__ bool has(int i) const { return NEXT ? first < D : at(i) < D; }
+  __device__ raw load(const TI* row) {
+    if constexpr (NEXT) {
+      uintptr_t a = reinterpret_cast<uintptr_t>(row);
+      asm("" : "+s"(a), "+v"(place[0]));
+      return *(const __attribute__((address_space(1))) typename Raw<TI, V>::type*)(
+          (const __attribute__((address_space(1))) char*)a + place[0]);
+    } else {
+      raw x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = __builtin_bit_cast(float, Row<TI>::load(row, place[i]));
+      return x;
+    }
+  }
+  __device__ Vals<V> widen(const raw& r) const {
+    if constexpr (NEXT) return ::widen<TI, V>(r);
+    else {
+      Vals<V> x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = Row<TI>::widen(__builtin_bit_cast(uint32_t, r[i]));
+      return x;
+    }
+  }
+  __device__ Vals<V> get(const TI* row) { return widen(load(row)); }
+  __device__ void put(TI* row, const Vals<V>& x) {
+    if constexpr (NEXT) store_vals<TI, V>(row + first, x);
+    else
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (has(i)) Row<TI>::store(row, place[i], x[i]);
+  }
+  // The same of fp32 vectors over the channels.
+  __device__ Vals<V> param(const float* p) const {
+    if constexpr (NEXT) return load_vals<float, V>(p + first);
+    else {
+      Vals<V> x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = p[min(at(i), D - 1)];
+      return x;
+    }
+  }
+};
+
 template <int W, int V>
 struct Taps {
   Vals<V> w[W], bias;
-  __device__ Taps(const ConvParams& p, int c0) {
-    // V W neighbouring floats; V is 1 or a multiple of 4
-    constexpr int E = V == 1 ? 1 : 4;
-    const float* at = p.w + (long)c0 * W;
+  template <typename TI, bool NEXT>
+  __device__ Taps(const ConvParams& p, const Channels<TI, V, NEXT>& ch) {
+    if constexpr (NEXT) {
+      // V W neighbouring floats; V is a multiple of 4
+      const float* at = p.w + (long)ch.first * W;
 #pragma unroll
-    for (int k = 0; k < V * W; k += E) {
-      const Vals<E> four = load_vals<float, E>(at + k);
+      for (int k = 0; k < V * W; k += 4) {
+        const Vals<4> four = load_vals<float, 4>(at + k);
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[(k + e) % W][(k + e) / W] = four[e];
+        for (int e = 0; e < 4; ++e) w[(k + e) % W][(k + e) / W] = four[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = p.w[(long)min(ch.at(i), p.D - 1) * W + j];
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = 0.f;
-    if (p.bias) bias = load_vals<float, V>(p.bias + c0);
+    if (p.bias) bias = ch.param(p.bias);
   }
   // The convolution at a token from the W - 1 before it and itself, oldest first.
   __device__ Vals<V> at(const Vals<V> (&before)[W - 1], const Vals<V>& x) const {
@@ -84,83 +150,84 @@ __device__ static inline void push(Vals<V> (&window)[W - 1], const Vals<V>& x) {
 
 // The W - 1 tokens before place t0 of a sequence whose first row is at x; the
 // ones before its first are h's, or zeros.
-template <typename TI, int W, int V>
-__device__ static inline void window_at(Vals<V> (&window)[W - 1], const TI* x, const TI* h, int t0, int D) {
+template <int W, typename TI, int V, bool NEXT>
+__device__ static inline void window_at(Vals<V> (&window)[W - 1], Channels<TI, V, NEXT>& ch, const TI* x, const TI* h,
+                                        int t0) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int t = t0 - (W - 1) + j;
-    if (t >= 0) window[j] = load_vals<TI, V>(x + (long)t * D);
-    else if (h) window[j] = load_vals<TI, V>(h + (long)(t + W - 1) * D);
+    if (t >= 0) window[j] = ch.get(x + (long)t * ch.D);
+    else if (h) window[j] = ch.get(h + (long)(t + W - 1) * ch.D);
     else
 #pragma unroll
       for (int i = 0; i < V; ++i) window[j][i] = 0.f;
   }
 }
 
-// Rows on their way at once.
+// Rows on their way at once (the backward pass of 4 x 4,096 x 1,280 bf16: 37 us
+// a call, 39 with two, 45 with eight).
 constexpr int FLIGHT = 4;
 
-template <typename TI, int W, int V>
+// A wave's unit: a segment (uniform, and the compiler is told so) and a tile.
+__device__ static inline long unit_of(const ConvParams& p) {
+  return (long)(blockIdx.x / p.tiles) * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+template <typename TI, int W, int V, bool NEXT>
 __global__ __launch_bounds__(64 * WAVES) void conv_kernel(const ConvParams p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long unit = (long)(blockIdx.x / p.tiles) * WAVES + wave;
+  const long unit = unit_of(p);
   if (unit >= p.segments) return;
   const Segment s = p.L ? segment_of(p.cu, p.B, p.T, p.L, p.nseg, unit) : sequence_of(p.cu, p.T, (int)unit);
   if (s.n < 0) return;
   int state = s.n;
-  if (p.slots) state = pool_slot(p.slots, p.nslots, s.n);
-  const int D = p.D, c0 = ((int)(blockIdx.x % p.tiles) * 64 + lane) * V;
-  if (c0 >= D) return;
-  const TI* x = static_cast<const TI*>(p.x) + s.row0 * D + c0;
-  TI* out = static_cast<TI*>(p.out) + s.row0 * D + c0;
+  if (p.slots) state = __builtin_amdgcn_readfirstlane(pool_slot(p.slots, p.nslots, s.n));
+  const int D = p.D;
+  Channels<TI, V, NEXT> ch(blockIdx.x % p.tiles, threadIdx.x & 63, D);
+  if (!ch.has(0)) return;
+  const TI* x = static_cast<const TI*>(p.x) + s.row0 * D;
+  TI* out = static_cast<TI*>(p.out) + s.row0 * D;
   if (state < 0) {
     Vals<V> zero;
 #pragma unroll
     for (int i = 0; i < V; ++i) zero[i] = 0.f;
-    for (int t = 0; t < s.len; ++t) store_vals<TI, V>(out + (long)t * D, zero);
+    for (int t = 0; t < s.len; ++t) ch.put(out + (long)t * D, zero);
     return;
   }
-  const long at = (long)state * (W - 1) * D + c0;
+  const long at = (long)state * (W - 1) * D;
   const TI* h = p.h0 ? static_cast<const TI*>(p.h0) + at : nullptr;
   Vals<V> window[W - 1];
-  window_at<TI, W, V>(window, x - (long)s.t0 * D, h, s.t0, D);
-  const Taps<W, V> taps(p, c0);
-  typename Raw<TI, V>::type next[FLIGHT];
+  window_at<W>(window, ch, x - (long)s.t0 * D, h, s.t0);
+  const Taps<W, V> taps(p, ch);
+  typename Channels<TI, V, NEXT>::raw next[FLIGHT];
 #pragma unroll
   for (int f = 0; f < FLIGHT; ++f)
-    if (f < s.len) next[f] = load_raw<TI, V>(x + (long)f * D);
-  for (int t = 0; t < s.len; t += FLIGHT) {
-    typename Raw<TI, V>::type now[FLIGHT];
-#pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      now[f] = next[f];
-      if (t + FLIGHT + f < s.len) next[f] = load_raw<TI, V>(x + (long)(t + FLIGHT + f) * D);
-    }
+    if (f < s.len) next[f] = ch.load(x + (long)f * D);
+  for (int t = 0; t < s.len; t += FLIGHT)
 #pragma unroll
     for (int f = 0; f < FLIGHT; ++f)
       if (t + f < s.len) {
-        const Vals<V> xv = widen<TI, V>(now[f]);
+        const Vals<V> xv = ch.widen(next[f]);
+        if (t + FLIGHT + f < s.len) next[f] = ch.load(x + (long)(t + FLIGHT + f) * D);
         Vals<V> y = taps.at(window, xv);
         if (p.silu)
 #pragma unroll
           for (int i = 0; i < V; ++i) y[i] *= sigmoid(y[i]);
-        store_vals<TI, V>(out + (long)(t + f) * D, y);
+        ch.put(out + (long)(t + f) * D, y);
         push<W, V>(window, xv);
       }
-  }
   if (s.last()) {
     TI* hT = static_cast<TI*>(p.hT) + at;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_vals<TI, V>(hT + (long)j * D, window[j]);
+    for (int j = 0; j < W - 1; ++j) ch.put(hT + (long)j * D, window[j]);
   }
 }
 
-template <typename TI, int W, int V>
+template <typename TI, int W, int V, bool NEXT>
 __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p) {
   __shared__ float sums[WAVES - 1][W + 1][64 * V];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int D = p.D, c0 = ((int)(blockIdx.x % p.tiles) * 64 + lane) * V;
-  const long unit = (long)(blockIdx.x / p.tiles) * WAVES + wave;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = p.D;
+  Channels<TI, V, NEXT> ch(blockIdx.x % p.tiles, lane, D);
+  const long unit = unit_of(p);
   Segment s = {0, -1, 0, 0, 0};
   if (unit < p.segments) s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, unit);
   Vals<V> dw[W], db;
@@ -170,40 +237,42 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
   }
-  if (s.n >= 0 && c0 < D) {
-    const TI* x = static_cast<const TI*>(p.x) + s.row0 * D + c0;
-    const TI* dout = static_cast<const TI*>(p.dout) + s.row0 * D + c0;
-    TI* dx = static_cast<TI*>(p.dx) + s.row0 * D + c0;
-    const long at = (long)s.n * (W - 1) * D + c0;
+  if (s.n >= 0 && ch.has(0)) {
+    const TI* x = static_cast<const TI*>(p.x) + s.row0 * D;
+    const TI* dout = static_cast<const TI*>(p.dout) + s.row0 * D;
+    TI* dx = static_cast<TI*>(p.dx) + s.row0 * D;
+    const long at = (long)s.n * (W - 1) * D;
     const TI* h = p.h0 ? static_cast<const TI*>(p.h0) + at : nullptr;
     const TI* dhT = p.dhT ? static_cast<const TI*>(p.dhT) + at : nullptr;
     TI* dh0 = p.dh0 ? static_cast<TI*>(p.dh0) + at : nullptr;
     Vals<V> window[W - 1], dys[W - 1];
-    window_at<TI, W, V>(window, x - (long)s.t0 * D, h, s.t0, D);
+    window_at<W>(window, ch, x - (long)s.t0 * D, h, s.t0);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) dys[j][i] = 0.f;
-    const Taps<W, V> taps(p, c0);
+    const Taps<W, V> taps(p, ch);
     // rows of the segment and, for their dx, the W - 1 that follow
-    const int rows = s.len + W - 1, there = s.total - s.t0;
-    typename Raw<TI, V>::type xn[FLIGHT], gn[FLIGHT];
+    const int rows = s.len + W - 1, there = s.total - s.t0, here = min(rows, there);
+    typename Channels<TI, V, NEXT>::raw xn[FLIGHT], gn[FLIGHT];
 #pragma unroll
     for (int f = 0; f < FLIGHT; ++f)
-      if (f < rows && f < there) {
-        xn[f] = load_raw<TI, V>(x + (long)f * D);
-        gn[f] = load_raw<TI, V>(dout + (long)f * D);
+      if (f < here) {
+        xn[f] = ch.load(x + (long)f * D);
+        gn[f] = ch.load(dout + (long)f * D);
       }
     for (int t = 0; t < rows; t += FLIGHT) {
-      typename Raw<TI, V>::type xr[FLIGHT], gr[FLIGHT];
+      // (all of a turn's loads at its beginning: 37 us a call, 43 where each row's
+      // follows the row before)
+      typename Channels<TI, V, NEXT>::raw xr[FLIGHT], gr[FLIGHT];
 #pragma unroll
       for (int f = 0; f < FLIGHT; ++f) {
         const int u = t + FLIGHT + f;
         xr[f] = xn[f];
         gr[f] = gn[f];
-        if (u < rows && u < there) {
-          xn[f] = load_raw<TI, V>(x + (long)u * D);
-          gn[f] = load_raw<TI, V>(dout + (long)u * D);
+        if (u < here) {
+          xn[f] = ch.load(x + (long)u * D);
+          gn[f] = ch.load(dout + (long)u * D);
         }
       }
 #pragma unroll
@@ -214,8 +283,8 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
 #pragma unroll
         for (int i = 0; i < V; ++i) dy[i] = xv[i] = 0.f;
         if (u < there) {
-          xv = widen<TI, V>(xr[f]);
-          dy = widen<TI, V>(gr[f]);
+          xv = ch.widen(xr[f]);
+          dy = ch.widen(gr[f]);
           if (p.silu) {
             const Vals<V> y = taps.at(window, xv);
 #pragma unroll
@@ -245,12 +314,12 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
           }
           const int k = e - (there - (W - 1));  // its place in the final state
           if (dhT && k >= 0) {
-            const Vals<V> more = load_vals<TI, V>(dhT + (long)k * D);
+            const Vals<V> more = ch.get(dhT + (long)k * D);
 #pragma unroll
             for (int i = 0; i < V; ++i) d[i] += more[i];
           }
-          if (e >= 0) store_vals<TI, V>(dx + (long)e * D, d);
-          else if (dh0) store_vals<TI, V>(dh0 + (long)u * D, d);
+          if (e >= 0) ch.put(dx + (long)e * D, d);
+          else if (dh0) ch.put(dh0 + (long)u * D, d);
         }
         push<W, V>(window, xv);
         push<W, V>(dys, dy);
@@ -266,8 +335,8 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
     }
   }
   __syncthreads();
-  if (wave == 0 && c0 < D) {
-    float* part = p.part + (long)(blockIdx.x / p.tiles) * (W + 1) * D + c0;
+  if (wave == 0 && ch.has(0)) {
+    float* part = p.part + (long)(blockIdx.x / p.tiles) * (W + 1) * D;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
       Vals<V> a = j < W ? dw[j < W ? j : 0] : db;
@@ -275,7 +344,11 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
       for (int k = 0; k < WAVES - 1; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) a[i] += sums[k][j][i * 64 + lane];
-      store_vals<float, V>(part + (long)j * D, a);
+      if constexpr (NEXT) store_vals<float, V>(part + (long)j * D + ch.first, a);
+      else
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (ch.has(i)) part[(long)j * D + ch.at(i)] = a[i];
     }
   }
 }
@@ -314,12 +387,20 @@ int rows_a_segment(long long rows, int D, int V, bool back) {
   return L;
 }
 
-// Channels a lane: 16 bytes of them forwards, 8 bytes of bf16 backwards (two
-// windows and the sums in registers), one where a row's start would not be
-// aligned.
-int channels(int D, int dtype, bool back) {
+// Channels a lane: 16 bytes of neighbours forwards, 8 bytes of bf16 backwards
+// (two windows and the sums in registers) where every row starts aligned to
+// them, else four, 64 apart (6 x 32,530 rows of 271 channels, W 3: 82 us forwards
+// and 120 backwards, 112 and 174 with one channel a lane), or one where there are
+// not more than a wave's.
+struct Width {
+  int V;
+  bool next;
+};
+
+Width channels(int D, int dtype, bool back) {
   const int want = dtype == GDN_F32 || back ? 4 : 8;
-  return D % want == 0 ? want : 1;
+  if (D % want == 0) return {want, true};
+  return {D > 64 ? 4 : 1, false};
 }
 
 int sizes_checked(int B, int T, int D, int W, bool packed, int dtype) {
@@ -349,20 +430,26 @@ bool plan(ConvParams& p, int V, bool back, bool whole, unsigned& grid) {
   return wgs < 1LL << 24;
 }
 
-template <typename TI, int V>
-void launch_fwd(const ConvParams& p, int W, unsigned grid, hipStream_t s) {
+template <typename TI, int V, bool NEXT, bool BACK>
+void launch(const ConvParams& p, int W, unsigned grid, hipStream_t s) {
   const dim3 g(grid), b(64 * WAVES);
-  if (W == 2) hipLaunchKernelGGL((conv_kernel<TI, 2, V>), g, b, 0, s, p);
-  else if (W == 3) hipLaunchKernelGGL((conv_kernel<TI, 3, V>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((conv_kernel<TI, 4, V>), g, b, 0, s, p);
+  if constexpr (BACK) {
+    if (W == 2) hipLaunchKernelGGL((conv_bwd_kernel<TI, 2, V, NEXT>), g, b, 0, s, p);
+    else if (W == 3) hipLaunchKernelGGL((conv_bwd_kernel<TI, 3, V, NEXT>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((conv_bwd_kernel<TI, 4, V, NEXT>), g, b, 0, s, p);
+  } else {
+    if (W == 2) hipLaunchKernelGGL((conv_kernel<TI, 2, V, NEXT>), g, b, 0, s, p);
+    else if (W == 3) hipLaunchKernelGGL((conv_kernel<TI, 3, V, NEXT>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((conv_kernel<TI, 4, V, NEXT>), g, b, 0, s, p);
+  }
 }
 
-template <typename TI, int V>
-void launch_bwd(const ConvParams& p, int W, unsigned grid, hipStream_t s) {
-  const dim3 g(grid), b(64 * WAVES);
-  if (W == 2) hipLaunchKernelGGL((conv_bwd_kernel<TI, 2, V>), g, b, 0, s, p);
-  else if (W == 3) hipLaunchKernelGGL((conv_bwd_kernel<TI, 3, V>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((conv_bwd_kernel<TI, 4, V>), g, b, 0, s, p);
+template <typename TI, bool BACK>
+void launch_width(const ConvParams& p, Width w, int W, unsigned grid, hipStream_t s) {
+  constexpr int MOST = BACK || sizeof(TI) == 4 ? 4 : 8;
+  if (w.next) launch<TI, MOST, true, BACK>(p, W, grid, s);
+  else if (w.V == 4) launch<TI, 4, false, BACK>(p, W, grid, s);
+  else launch<TI, 1, false, BACK>(p, W, grid, s);
 }
 
 int forward(ConvParams p, int W, int dtype, int flags, void* stream) {
@@ -381,13 +468,12 @@ int forward(ConvParams p, int W, int dtype, int flags, void* stream) {
     return GDN_ERR_INVALID_ARG;
   if (p.B == 0) return GDN_OK;
   p.silu = flags & GDN_CONV_SILU;
-  const int V = channels(p.D, dtype, false);
+  const Width w = channels(p.D, dtype, false);
   unsigned grid;
   // in place a later segment could write a state that the first one reads
-  if (!plan(p, V, false, pooled || p.h0 == p.hT, grid)) return GDN_ERR_INVALID_ARG;
+  if (!plan(p, w.V, false, pooled || p.h0 == p.hT, grid)) return GDN_ERR_INVALID_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dtype == GDN_BF16) V == 8 ? launch_fwd<__bf16, 8>(p, W, grid, s) : launch_fwd<__bf16, 1>(p, W, grid, s);
-  else V == 4 ? launch_fwd<float, 4>(p, W, grid, s) : launch_fwd<float, 1>(p, W, grid, s);
+  dtype == GDN_BF16 ? launch_width<__bf16, false>(p, w, W, grid, s) : launch_width<float, false>(p, w, W, grid, s);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -419,7 +505,7 @@ extern "C" long long gdn_conv_workspace_size(int B, int T, int D, int W, int pac
   p.B = B; p.T = T; p.D = D;
   p.cu = packed ? reinterpret_cast<const int32_t*>(16) : nullptr;  // only asked whether there is one
   unsigned grid;
-  if (!plan(p, channels(D, dtype, true), true, false, grid)) return GDN_ERR_INVALID_ARG;
+  if (!plan(p, channels(D, dtype, true).V, true, false, grid)) return GDN_ERR_INVALID_ARG;
   return (long long)(grid / p.tiles) * (W + 1) * D * 4;
 }
 
@@ -448,13 +534,12 @@ extern "C" int gdn_conv_bwd(const void* x, const float* w, const float* bias, co
   p.part = static_cast<float*>(workspace);
   p.B = B; p.T = T; p.D = D;
   p.silu = flags & GDN_CONV_SILU;
-  const int V = channels(D, dtype, true);
+  const Width v = channels(D, dtype, true);
   unsigned grid;
-  if (!plan(p, V, true, false, grid)) return GDN_ERR_INVALID_ARG;
+  if (!plan(p, v.V, true, false, grid)) return GDN_ERR_INVALID_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (grid > 0) {
-    if (dtype == GDN_BF16) V == 4 ? launch_bwd<__bf16, 4>(p, W, grid, s) : launch_bwd<__bf16, 1>(p, W, grid, s);
-    else V == 4 ? launch_bwd<float, 4>(p, W, grid, s) : launch_bwd<float, 1>(p, W, grid, s);
+    dtype == GDN_BF16 ? launch_width<__bf16, true>(p, v, W, grid, s) : launch_width<float, true>(p, v, W, grid, s);
   }
   const long long cols = (long long)(W + 1) * D;
   hipLaunchKernelGGL(conv_weights_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, p.part,

@@ -74,6 +74,40 @@ __device__ static inline void store_vals(TI* p, const Vals<V>& x) {
   }
 }
 
+template <int BYTES>
+struct Bits {
+  typedef uint32_t type;
+};
+template <>
+struct Bits<2> {
+  typedef uint16_t type;
+};
+
+// A lane's value in a row of one of the token tensors.  The row's address, the
+// same in all lanes, is kept in scalar registers (the assembly is empty; without
+// it the sum is formed in vector registers, three instructions a load), and the
+// value in 32 bits (two of 16 would be packed, and waited for, on the way).
+template <typename TI>
+struct Row {
+  typedef typename Bits<sizeof(TI)>::type bits;
+  typedef __attribute__((address_space(1))) bits* place;
+  __device__ static place at(const TI* row, uint32_t& lane) {
+    uintptr_t a = reinterpret_cast<uintptr_t>(row);
+    asm("" : "+s"(a), "+v"(lane));
+    return (place)((__attribute__((address_space(1))) char*)a + lane);
+  }
+  __device__ static uint32_t load(const TI* row, uint32_t& lane) { return *at(row, lane); }
+  __device__ static void store(TI* row, uint32_t& lane, float x) { *at(row, lane) = __builtin_bit_cast(bits, (TI)x); }
+  // Of the lanes whose place is inside the row of `bytes` bytes, without a branch.
+  __device__ static void store_inside(TI* row, int bytes, uint32_t lane, float x) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(row, 0, bytes, 0x00020000);
+    const bits b = __builtin_bit_cast(bits, (TI)x);
+    if constexpr (sizeof(TI) == 2) __builtin_amdgcn_raw_buffer_store_b16(b, r, lane, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(b, r, lane, 0, 0);
+  }
+  __device__ static float widen(uint32_t x) { return __builtin_bit_cast(float, sizeof(TI) == 2 ? x << 16 : x); }
+};
+
 // --------------------------------------------------------------- functions --
 
 // 1 / (1 + exp(-x)); exp2 and the reciprocal are within 1 ulp, the product

@@ -115,7 +115,11 @@ def _call(name, dev, *args):
     import torch
 
     fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
+    try:
+        here = torch._C._cuda_getDevice()  # the tensors are there: nothing is left to initialise
+    except AttributeError:
+        here = torch.cuda.current_device()
+    if here == dev.index:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):

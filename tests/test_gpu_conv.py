@@ -56,7 +56,7 @@ def test_lengths_and_widths(dtype, W, T):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("D", [1, 7, 8, 12, 63, 130, 512, 520])
+@pytest.mark.parametrize("D", [1, 7, 8, 12, 63, 64, 65, 130, 193, 257, 300, 512, 520, 577])
 def test_channels(dtype, D):
     both(*make(D, dtype, [19] * 2, D, 4, False), dtype)
 
