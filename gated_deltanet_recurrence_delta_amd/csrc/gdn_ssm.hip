@@ -412,15 +412,28 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
     dn[k] = dt[o];
     zn[k] = z[o];
 #pragma unroll
-    for (int f = 0; f < TOKENS; ++f)
-      if (t + f < len) {
-        bn[k][f] = load_raw<TI, 4>(bk + (t + f) * KS);
-        cn[k][f] = load_raw<TI, 4>(ck + (t + f) * KS);
-      }
+    for (int f = 0; f < TOKENS; ++f) {
+      const long u = min(t + f, len - 1) * KS;
+      bn[k][f] = load_raw<TI, 4>(bk + u);
+      cn[k][f] = load_raw<TI, 4>(ck + u);
+    }
   };
+  // What a turn's tokens need of their own: formed while the turn before is
+  // worked on.  Tokens behind the last take a step of zero.
+  struct Own {
+    float step, u, skip, gate;
+  };
+  auto own_of = [&](int k, int t) {
+    const float xv = (float)xn[k], zv = (float)zn[k], step = step_of((float)dn[k] + bias, p.softplus);
+    const float gate = zv * sigmoid(zv), st = t + own < len ? step : 0.f;
+    return Own{st, st * xv, skip * xv, p.z ? gate : 1.f};
+  };
+  Own now = {0.f, 0.f, 0.f, 0.f};
+  if (len > 0) {
 #pragma unroll
-  for (int k = 0; k < TURNS; ++k)
-    if (TOKENS * k < len) load(k, TOKENS * k);
+    for (int k = 0; k < TURNS; ++k) load(k, TOKENS * k);
+    now = own_of(0, 0);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) A[i] = -LOG2E * expf(A[i]);
   for (int t0 = 0; t0 < len; t0 += TOKENS * TURNS)
@@ -428,27 +441,28 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
     for (int k = 0; k < TURNS; ++k) {
       const int t = t0 + TOKENS * k;
       if (t >= len) break;
-      const float xv = (float)xn[k], zv = (float)zn[k];
-      const float st = step_of((float)dn[k] + bias, p.softplus);
-      const Vals<4> sv = TOKENS == 1 ? Vals<4>{{st}} : quad(st), uv = TOKENS == 1 ? Vals<4>{{st * xv}} : quad(st * xv);
       Vals<4> b[TOKENS], c[TOKENS], y = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int f = 0; f < TOKENS; ++f) {
         b[f] = widen<TI, 4>(bn[k][f]);
         c[f] = widen<TI, 4>(cn[k][f]);
       }
-      if (t + TOKENS * TURNS < len) load(k, t + TOKENS * TURNS);
+      const Own own_now = now;
+      if (t + TOKENS * TURNS < len) {
+        load(k, t + TOKENS * TURNS);
+        if constexpr (TURNS == 1) now = own_of(0, t + TOKENS);
+      }
+      if constexpr (TURNS > 1) now = own_of((k + 1) % TURNS, t + TOKENS);
+      const Vals<4> sv = TOKENS == 1 ? Vals<4>{{own_now.step}} : quad(own_now.step);
+      const Vals<4> uv = TOKENS == 1 ? Vals<4>{{own_now.u}} : quad(own_now.u);
 #pragma unroll
-      for (int f = 0; f < TOKENS; ++f) {
-        if (t + f >= len) break;
+      for (int f = 0; f < TOKENS; ++f)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sv[f] * A[i]), h[i], uv[f] * b[f][i]);
           y[f] = __builtin_fmaf(c[f][i], h[i], y[f]);
         }
-      }
-      float o = __builtin_fmaf(skip, xv, TOKENS == 1 ? sum_lanes<LC>(y[0]) : sum_own<LC>(y, odd, high));
-      if (p.z) o *= zv * sigmoid(zv);
+      const float o = (own_now.skip + (TOKENS == 1 ? sum_lanes<LC>(y[0]) : sum_own<LC>(y, odd, high))) * own_now.gate;
       if (slice < TOKENS && t + own < len) out[(long)(t + own) * D] = (TI)o;
     }
   store_vals<float, 4>(p.hT + sat, h);
