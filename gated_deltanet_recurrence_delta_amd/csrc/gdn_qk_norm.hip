@@ -231,7 +231,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormParams p) {
 }
 
 // The partial sums' sums: 32 channels of one side a workgroup, 32 threads each
-// (one workgroup a side took 14 us for 2,048 rows of 128; these X).
+// (one workgroup a side took 14 us for 2,048 rows of 128, these 5).
 __global__ __launch_bounds__(1024) void norm_weights_kernel(const NormParams p, int d, float* dwq, float* dwk) {
   __shared__ float sums[32][32];
   const int side = blockIdx.y, c = threadIdx.x & 31, k = threadIdx.x >> 5;

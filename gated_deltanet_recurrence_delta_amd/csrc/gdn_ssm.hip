@@ -83,6 +83,14 @@ __device__ static inline float step_of(float v, int soft) {
   return soft ? s : v;
 }
 
+// A times log2(e), for decays as powers of two.  A finite number even where
+// exp(A_log) is none: a step of zero (which tokens behind a segment's last take)
+// leaves a state as it is.
+__device__ static inline float rate_of(float A_log) {
+  const float a = -LOG2E * expf(A_log);
+  return a < -3e38f ? -3e38f : a;
+}
+
 // -------------------------------------------------------------------- keys --
 
 // Sixteen values of a token's key through the scalar unit: the address is the
@@ -178,7 +186,7 @@ __global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
   load_states<N>(A, p.A_log + (long)d * N);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    A[i] = -LOG2E * expf(A[i]);
+    A[i] = rate_of(A[i]);
     h[i] = 0.f;
   }
   if constexpr (OUTPUT) {
@@ -289,7 +297,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
       slot = b / p.L + n;
       count = (int)min((long)(e - b + p.L - 1) / p.L, max(p.segments - slot, 0L));
     }
-    const float A = -LOG2E * expf(p.A_log[r]);
+    const float A = rate_of(p.A_log[r]);
     float* state = (back ? p.R : p.E) + r;
     const float* first = back ? p.dhT : p.h0;
     const int part = (count + GROUPS - 1) / GROUPS, i0 = min(group * part, count), i1 = min(i0 + part, count);
@@ -375,8 +383,9 @@ __device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
 // them comes by DPP, so that a token costs a lane some 45 instructions, not 95.
 // TURNS turns are on their way at once.
 //
-// Bound by memory for one token each (X us, Y floor: 128 sequences, 1,280
-// channels); for longer sequences of few channels by one wave's instructions.
+// Bound by memory for one token each (128 sequences, 1,280 channels: 8.2 us, 4.7
+// at a large copy's rate); for longer sequences of few channels by one wave's
+// instructions, some 0.13 us a token.
 template <typename TI, int N, int TURNS, int TOKENS>
 __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
   constexpr int LC = N / 4, CH = 256 / LC;
@@ -435,7 +444,7 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
     now = own_of(0, 0);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = -LOG2E * expf(A[i]);
+  for (int i = 0; i < 4; ++i) A[i] = rate_of(A[i]);
   for (int t0 = 0; t0 < len; t0 += TOKENS * TURNS)
 #pragma unroll
     for (int k = 0; k < TURNS; ++k) {
@@ -492,7 +501,7 @@ __device__ static inline void bwd_map(const SsmParams& p, long k, int tiles, int
   load_states<16>(A, p.A_log + (long)d * N + part * 16);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    A[i] = -LOG2E * expf(A[i]);
+    A[i] = rate_of(A[i]);
     E[i] = R[i] = 0.f;
     P[i] = 1.f;
   }
@@ -624,7 +633,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmParams 
   const int own = g * p.Dg + min(cown, p.Dg - 1);
   // places in a row of channels (bytes) and in a segment's states (floats)
   uint32_t lane_at = (uint32_t)own * sizeof(TI), state_at[4];
-  const uint32_t mine_at = mine ? lane_at : ~0u;
+  const uint32_t mine_at = mine ? lane_at : 1u << 30;  // (no row has that many bytes)
 #pragma unroll
   for (int c = 0; c < 4; ++c) state_at[c] = (uint32_t)(g * p.Dg + min(c0 + c, p.Dg - 1)) * N + slice * 4;
 
@@ -634,7 +643,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmParams 
     const Vals<4> a = load_vals<float, 4>(p.A_log + state_at[c]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      A[c][j] = -LOG2E * expf(a[j]);
+      A[c][j] = rate_of(a[j]);
       dA[c][j] = 0.f;
     }
   }
@@ -942,7 +951,9 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   const long long segments = std::max(1LL, packed ? WAVES / tiles - B / 2 : WAVES / chains * B);
   long long L = (rows + segments - 1) / segments;
   if (!packed) L = (T + segments / B - 1) / (segments / B);
-  c.L = (int)std::max(32LL, (L + FLIGHT - 1) / FLIGHT * FLIGHT);
+  // (2 x 2,013 x 96, N 64: 64 us with 20 rows at least, 86 with 32, 66 with 12; 4
+  // x 1,000 x 512, N 16: 42, 40, 44)
+  c.L = (int)std::max(20LL, (L + FLIGHT - 1) / FLIGHT * FLIGHT);
   if (c.L >= T) {
     c.L = T;
     return c;

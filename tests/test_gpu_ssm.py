@@ -159,6 +159,21 @@ def test_steps_so_large_that_nothing_is_left():
     check_backward(t, c, "f32")
 
 
+@pytest.mark.parametrize("T", [3, 70, 201, 402])
+def test_rates_beyond_the_numbers(T):
+    """exp(A_log) infinite: nothing is remembered; zero: nothing is forgotten."""
+    t, c = make(20, "f32", [T], 20, 1, 16, False)
+    t["A_log"][:, 0], t["A_log"][:, 1] = 100.0, -200.0
+    c["A_log"][:, 0], c["A_log"][:, 1] = 100.0, -200.0
+    check_forward(t, c, "f32")
+    g = backward(t)
+    ok = torch.ones(16, dtype=torch.bool, device="cuda")
+    ok[0] = False
+    for n in ("dx", "ddt", "db", "dc", "dD", "dz", "ddt_bias", "dh0"):
+        assert g[n].isfinite().all(), n
+    assert g["dA_log"][:, ok].isfinite().all() and not g["dA_log"][:, 1].any()
+
+
 @pytest.mark.parametrize("T", [30, 200])
 def test_rows_of_no_sequence_are_left(T):
     t, c = make(6, "bf16", [T], 40, 1, 16, True)
