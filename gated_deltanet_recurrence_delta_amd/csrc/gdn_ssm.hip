@@ -302,6 +302,8 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
     const float* first = back ? p.dhT : p.h0;
     const int part = (count + GROUPS - 1) / GROUPS, i0 = min(group * part, count), i1 = min(i0 + part, count);
     const long step = back ? -1 : 1, begin = back ? slot + count - 1 : slot;
+    // (read before the parts meet: the last part's thread writes dh0, which may be dhT itself)
+    const float begun = first ? first[id] : 0.f;
     float h = 0.f, e[F], s[F];
     auto load = [&](int i) {
 #pragma unroll
@@ -327,7 +329,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
       sums[group][lane] = S;
       __syncthreads();
     }
-    h = first ? first[id] : 0.f;
+    h = begun;
     if constexpr (GROUPS > 1)
       for (int g = 0; g < group; ++g) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * sums[g][lane]), h, ends[g][lane]);
     if (id0 + lane >= p.B * DN) continue;

@@ -392,3 +392,24 @@ def test_twice_the_same():
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     a, b = backward(t), backward(t)
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_state_gradients_in_place():
+    """dh0 in dhT's place, few states of many segments: the join's threads share them."""
+    t, _ = make(31, "bf16", [1800], 40, 1, 16, False)
+    want = backward(t)
+    a, o = args(t)
+    D, N = 40, 16
+    size = gdn.gdn_ssm_workspace_size(1, 1800, D, 1, N, False, gdn.GDN_BF16, True)
+    for _ in range(3):
+        g = {n: torch.empty_like(want[n]) for n in want}
+        g["dh0"] = t["dhT"].clone()
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        ptr = lambda v: 0 if v is None else v.data_ptr()  # noqa: E731
+        rc = gdn.gdn_ssm_bwd(*(ptr(v) for v in (*a, o["D"], o["z"], o["dt_bias"], o["h0"], None, t["dout"], g["dh0"])),
+                             *(ptr(g[n]) for n in ("dx", "ddt", "db", "dc", "dA_log", "dD", "dz", "ddt_bias", "dh0")),
+                             1, 1800, D, 1, N, torch.cuda.current_stream().cuda_stream, gdn.GDN_BF16, 1, ptr(ws), size)
+        assert rc == 0
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(g[n], want[n]), n
