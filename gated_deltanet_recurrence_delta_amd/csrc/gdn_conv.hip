@@ -2,9 +2,10 @@
 // and on states in a pool, for gfx950.
 //
 // A lane owns V channels -- neighbours, 16 bytes of them, where D allows, else
-// 64 apart, so that a wave's loads are whole lines at any alignment -- and walks down a segment of its sequence with the last W - 1 tokens in
-// registers, so that a token is read once and, at a segment's start, W - 1 of
-// them a second time.  Bound by memory: x in, out out.
+// 64 apart, so that a wave's loads are whole lines at any alignment -- and walks
+// down a segment of its sequence with the last W - 1 tokens in registers, so that
+// a token is read once and, at a segment's start, W - 1 of them a second time.
+// Bound by memory: x in, out out.
 //
 // Backwards the convolution is formed again (dy needs y), and a second window
 // holds the last W - 1 dy: a token's dx is complete W - 1 tokens later, so a
@@ -215,7 +216,9 @@ __global__ __launch_bounds__(64 * WAVES) void conv_kernel(const ConvParams p) {
         ch.put(out + (long)(t + f) * D, y);
         push<W, V>(window, xv);
       }
-  if (s.last()) {
+  // The final state, by the wave that has read the initial one: hT may be h0.
+  if (s.first()) {
+    if (!s.last()) window_at<W>(window, ch, x, h, s.total);
     TI* hT = static_cast<TI*>(p.hT) + at;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) ch.put(hT + (long)j * D, window[j]);
@@ -470,8 +473,7 @@ int forward(ConvParams p, int W, int dtype, int flags, void* stream) {
   p.silu = flags & GDN_CONV_SILU;
   const Width w = channels(p.D, dtype, false);
   unsigned grid;
-  // in place a later segment could write a state that the first one reads
-  if (!plan(p, w.V, false, pooled || p.h0 == p.hT, grid)) return GDN_ERR_INVALID_ARG;
+  if (!plan(p, w.V, false, pooled, grid)) return GDN_ERR_INVALID_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   dtype == GDN_BF16 ? launch_width<__bf16, false>(p, w, W, grid, s) : launch_width<float, false>(p, w, W, grid, s);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;

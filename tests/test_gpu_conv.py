@@ -248,3 +248,15 @@ def test_twice_the_same():
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     a, b = backward(t), backward(t)
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_in_place_states_of_cut_sequences(packed):
+    """hT in h0's place where the first segment reads what another one would write."""
+    for dtype, W in (("bf16", 4), ("f32", 2)):
+        t, _ = make(21, dtype, [700, 700, 1, 2, 0, 3] if packed else [700] * 3, 520, W, packed)
+        out, hT = forward(t)
+        for _ in range(3):
+            h = t["h0"].clone()
+            o, h2 = gdn.conv_fwd(t["x"], t["w"], t["bias"], h, t["cu_seqlens"], hT=h)
+            assert h2 is h and torch.equal(h, hT) and torch.equal(o, out)
