@@ -77,6 +77,12 @@ def _batch(name, t, cu_seqlens, dims):
     return cu_seqlens.numel() - 1, shape[0]
 
 
+def _flat(t):
+    """A gradient contiguous and at an address that the kernels take: autograd's may be a part of a larger tensor."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _optional(name, t, shape, dtype):
     if t is not None:
         _like(name, t, shape, dtype)
@@ -224,7 +230,7 @@ def causal_conv(x, w, bias=None, h0=None, cu_seqlens=None, silu=True):
             @torch.autograd.function.once_differentiable
             def backward(ctx, dout, dhT):
                 x, w, bias, h0, cu_seqlens = ctx.saved_tensors
-                g = _backward(x, w, dout.contiguous(), bias, h0, cu_seqlens, dhT.contiguous(), ctx.silu,
+                g = _backward(x, w, _flat(dout), bias, h0, cu_seqlens, _flat(dhT), ctx.silu,
                               h0 is not None, None, None, cu_seqlens is not None)
                 return g["dx"], g["dw"], g["dbias"], g["dh0"], None, None
 

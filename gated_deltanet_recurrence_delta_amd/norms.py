@@ -6,7 +6,7 @@ in the package's other entry points.
 from __future__ import annotations
 
 from . import load
-from .conv import _storage
+from .conv import _flat, _storage
 from .linear import _call, _like, _placed, _ptr, _raw_stream, _scratch
 
 __all__ = ["gdn_qk_norm_fwd", "gdn_qk_norm_bwd", "gdn_qk_norm_workspace_size", "qk_norm_fwd", "qk_norm_bwd", "qk_norm"]
@@ -152,7 +152,7 @@ def qk_norm(q, k, cos=None, sin=None, pos=None, wq=None, wk=None, norm="rms", ep
             @torch.autograd.function.once_differentiable
             def backward(ctx, dqo, dko):
                 q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
-                g = qk_norm_bwd(q, k, dqo.contiguous(), dko.contiguous(), cos, sin, pos, wq, wk, *ctx.how)
+                g = qk_norm_bwd(q, k, _flat(dqo), _flat(dko), cos, sin, pos, wq, wk, *ctx.how)
                 return g["dq"], g["dk"], g["dwq"], g["dwk"], None, None, None, None, None, None
 
         _NORM = _QkNorm

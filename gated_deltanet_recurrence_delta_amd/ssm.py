@@ -11,7 +11,7 @@ from __future__ import annotations
 import functools
 
 from . import load
-from .conv import _batch, _optional, _pool_of, _storage
+from .conv import _batch, _flat, _optional, _pool_of, _storage
 from .linear import _call, _like, _placed, _ptr, _raw_stream, _scratch
 
 __all__ = ["gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_workspace_size", "gdn_ssm_fwd_recurrent_pool", "ssm_fwd", "ssm_bwd",
@@ -213,7 +213,7 @@ def selective_scan(x, dt, b, c, A_log, D=None, z=None, dt_bias=None, h0=None, cu
             @torch.autograd.function.once_differentiable
             def backward(ctx, dout, dhT):
                 x, dt, b, c, A_log, D, z, dt_bias, h0, cu_seqlens = ctx.saved_tensors
-                g = _backward(x, dt, b, c, A_log, dout.contiguous(), D, z, dt_bias, h0, cu_seqlens, dhT.contiguous(),
+                g = _backward(x, dt, b, c, A_log, _flat(dout), D, z, dt_bias, h0, cu_seqlens, _flat(dhT),
                               ctx.softplus, h0 is not None, None, None, cu_seqlens is not None)
                 return (*(g[n] for n in ("dx", "ddt", "db", "dc", "dA_log", "dD", "dz", "ddt_bias", "dh0")), None,
                         None)

@@ -260,3 +260,18 @@ def test_in_place_states_of_cut_sequences(packed):
             h = t["h0"].clone()
             o, h2 = gdn.conv_fwd(t["x"], t["w"], t["bias"], h, t["cu_seqlens"], hT=h)
             assert h2 is h and torch.equal(h, hT) and torch.equal(o, out)
+
+
+def test_gradients_that_start_anywhere():
+    """A gradient that autograd gives as a part of a larger tensor."""
+    t, _ = make(22, "bf16", [3, 4], 7, 3, True)
+    want = backward(t)
+    leaves = [t[n].requires_grad_() for n in ("x", "w", "bias", "h0")]
+    out, hT = gdn.causal_conv(*leaves, t["cu_seqlens"])
+    both = torch.cat([torch.zeros(1, 7, dtype=out.dtype, device="cuda"), out])
+    states = torch.cat([torch.zeros(1, 2, 7, dtype=out.dtype, device="cuda"), hT])
+    first = torch.zeros_like(both[:1])
+    got = torch.autograd.grad([both, states], leaves,
+                              [torch.cat([first, t["dout"]]), torch.cat([torch.zeros_like(states[:1]), t["dhT"]])])
+    for a, n in zip(got, ("dx", "dw", "dbias", "dh0")):
+        assert torch.equal(a, want[n]), n

@@ -413,3 +413,16 @@ def test_state_gradients_in_place():
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(g[n], want[n]), n
+
+
+def test_gradients_that_start_anywhere():
+    """A gradient that autograd gives as a part of a larger tensor."""
+    t, _ = make(32, "bf16", [3, 4], 7, 1, 16, True)
+    want = backward(t)
+    a, o = args(t)
+    leaves = [v.requires_grad_() for v in (*a, o["D"], o["z"], o["dt_bias"], o["h0"])]
+    out, hT = gdn.selective_scan(*leaves, t["cu_seqlens"])
+    both = torch.cat([torch.zeros(1, 7, dtype=out.dtype, device="cuda"), out])
+    got = torch.autograd.grad([both, hT], leaves, [torch.cat([torch.zeros_like(both[:1]), t["dout"]]), t["dhT"]])
+    for v, n in zip(got, ("dx", "ddt", "db", "dc", "dA_log", "dD", "dz", "ddt_bias", "dh0")):
+        assert torch.equal(v, want[n]), n
