@@ -180,24 +180,26 @@ __global__ __launch_bounds__(64 * WAVES) void conv_kernel(const ConvParams p) {
   if (unit >= p.segments) return;
   const Segment s = p.L ? segment_of(p.cu, p.B, p.T, p.L, p.nseg, unit) : sequence_of(p.cu, p.T, (int)unit);
   if (s.n < 0) return;
-  int state = s.n;
-  if (p.slots) state = __builtin_amdgcn_readfirstlane(pool_slot(p.slots, p.nslots, s.n));
+  SlotSearch search = p.slots ? SlotSearch(p.slots, s.n) : SlotSearch();
   const int D = p.D;
   Channels<TI, V, NEXT> ch(blockIdx.x % p.tiles, threadIdx.x & 63, D);
-  if (!ch.has(0)) return;
+  const bool inside = ch.has(0);
   const TI* x = static_cast<const TI*>(p.x) + s.row0 * D;
   TI* out = static_cast<TI*>(p.out) + s.row0 * D;
-  if (state < 0) {
+  // The state is on its way while its slot is looked for among the earlier ones.
+  const long at = (long)(p.slots ? __builtin_amdgcn_readfirstlane(search.slot) : s.n) * (W - 1) * D;
+  const TI* h = p.h0 && (!p.slots || search.in(p.nslots)) ? static_cast<const TI*>(p.h0) + at : nullptr;
+  Vals<V> window[W - 1];
+  if (inside) window_at<W>(window, ch, x - (long)s.t0 * D, h, s.t0);
+  const bool known = !p.slots || search.own(p.slots, p.nslots, s.n);
+  if (!inside) return;
+  if (!known) {
     Vals<V> zero;
 #pragma unroll
     for (int i = 0; i < V; ++i) zero[i] = 0.f;
     for (int t = 0; t < s.len; ++t) ch.put(out + (long)t * D, zero);
     return;
   }
-  const long at = (long)state * (W - 1) * D;
-  const TI* h = p.h0 ? static_cast<const TI*>(p.h0) + at : nullptr;
-  Vals<V> window[W - 1];
-  window_at<W>(window, ch, x - (long)s.t0 * D, h, s.t0);
   const Taps<W, V> taps(p, ch);
   typename Channels<TI, V, NEXT>::raw next[FLIGHT];
 #pragma unroll

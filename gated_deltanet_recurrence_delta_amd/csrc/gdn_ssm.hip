@@ -22,6 +22,8 @@
 
 namespace {
 
+typedef float f4 __attribute__((ext_vector_type(4)));
+
 constexpr float LOG2E = 1.44269504f;
 
 struct SsmParams {
@@ -385,10 +387,10 @@ __device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
 // them comes by DPP, so that a token costs a lane some 45 instructions, not 95.
 // TURNS turns are on their way at once.
 //
-// Bound by memory for one token each (128 sequences, 1,280 channels: 8.2 us, 4.7
-// at a large copy's rate); for longer sequences of few channels by one wave's
-// instructions, some 0.13 us a token.
-template <typename TI, int N, int TURNS, int TOKENS>
+// Bound by memory for one token each (N 16: 128 sequences of 1,280 channels 7.9 us,
+// 4.7 at a large copy's rate; 512 of 2,560 channels 42 us, 37 at that rate); for
+// longer sequences of few channels by one wave's instructions, some 0.13 us a token.
+template <typename TI, int N, int TURNS, int TOKENS, bool STREAM>
 __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
   constexpr int LC = N / 4, CH = 256 / LC;
   const int tiles = (p.D + CH - 1) / CH;
@@ -396,19 +398,25 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
   const int slice = threadIdx.x % LC, d = tile * CH + threadIdx.x / LC, own = slice & (TOKENS - 1);
   const bool odd = slice & 1, high = slice & 2;
   const Segment s = sequence_of(p.cu, p.T, n);
-  int state = n;
-  if (p.slots) state = pool_slot(p.slots, p.nslots, n);
-  if (d >= p.D) return;
   const int D = p.D, len = s.len;
-  TI* out = static_cast<TI*>(p.out) + s.row0 * D + d;
-  if (state < 0) {
-    for (int t = slice; t < len; t += LC) out[(long)t * D] = (TI)0.f;
-    return;
+  const bool inside = d < D;
+  // The state is on its way while its slot is looked for among the earlier ones.
+  SlotSearch search = p.slots ? SlotSearch(p.slots, n) : SlotSearch();
+  const long sat = ((long)(p.slots ? search.slot : n) * D + d) * N + slice * 4;
+  Vals<4> h = {{0.f, 0.f, 0.f, 0.f}}, A = h;
+  float bias = 0.f, skip = 0.f;
+  if (inside) {
+    if (p.h0 && (!p.slots || search.in(p.nslots))) {
+      const f4* from = reinterpret_cast<const f4*>(p.h0 + sat);
+      f4 q;
+      if constexpr (STREAM) q = __builtin_nontemporal_load(from);
+      else q = *from;
+      h = Vals<4>{{q[0], q[1], q[2], q[3]}};
+    }
+    A = load_vals<float, 4>(p.A_log + (long)d * N + slice * 4);
+    if (p.dt_bias) bias = p.dt_bias[d];
+    if (p.Dskip) skip = p.Dskip[d];
   }
-  const long sat = ((long)state * D + d) * N + slice * 4;
-  Vals<4> h = {{0.f, 0.f, 0.f, 0.f}}, A = load_vals<float, 4>(p.A_log + (long)d * N + slice * 4);
-  if (p.h0) h = load_vals<float, 4>(p.h0 + sat);
-  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.Dskip ? p.Dskip[d] : 0.f;
   const TI* x = static_cast<const TI*>(p.x) + s.row0 * D + d;
   const TI* dt = static_cast<const TI*>(p.dt) + s.row0 * D + d;
   const TI* z = p.z ? static_cast<const TI*>(p.z) + s.row0 * D + d : x;
@@ -434,17 +442,23 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
   struct Own {
     float step, u, skip, gate;
   };
+  if (inside && len > 0)
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) load(k, TOKENS * k);
+  const bool known = !p.slots || search.own(p.slots, p.nslots, n);
+  if (!inside) return;
+  TI* out = static_cast<TI*>(p.out) + s.row0 * D + d;
+  if (!known) {
+    for (int t = slice; t < len; t += LC) out[(long)t * D] = (TI)0.f;
+    return;
+  }
   auto own_of = [&](int k, int t) {
     const float xv = (float)xn[k], zv = (float)zn[k], step = step_of((float)dn[k] + bias, p.softplus);
     const float gate = zv * sigmoid(zv), st = t + own < len ? step : 0.f;
     return Own{st, st * xv, skip * xv, p.z ? gate : 1.f};
   };
   Own now = {0.f, 0.f, 0.f, 0.f};
-  if (len > 0) {
-#pragma unroll
-    for (int k = 0; k < TURNS; ++k) load(k, TOKENS * k);
-    now = own_of(0, 0);
-  }
+  if (len > 0) now = own_of(0, 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) A[i] = rate_of(A[i]);
   for (int t0 = 0; t0 < len; t0 += TOKENS * TURNS)
@@ -476,7 +490,10 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
       const float o = (own_now.skip + (TOKENS == 1 ? sum_lanes<LC>(y[0]) : sum_own<LC>(y, odd, high))) * own_now.gate;
       if (slice < TOKENS && t + own < len) out[(long)(t + own) * D] = (TI)o;
     }
-  store_vals<float, 4>(p.hT + sat, h);
+  f4* to = reinterpret_cast<f4*>(p.hT + sat);
+  const f4 q = {h[0], h[1], h[2], h[3]};
+  if constexpr (STREAM) __builtin_nontemporal_store(q, to);
+  else *to = q;
 }
 
 // ---------------------------------------------------------------- backwards --
@@ -1044,13 +1061,22 @@ void launch_join(const SsmParams& p, long long states, int directions, hipStream
 
 // Two turns of four tokens in flight, one where sequences have no more, and
 // turns of a single token where they have that: fewer registers, more waves (one
-// token of 128 sequences, 1,280 channels: 7.9 us against 9.5).
+// token of 128 sequences, 1,280 channels: 7.9 us against 9.5).  More states than
+// the eight second-level caches hold (32 MB) then go past them, read and written
+// (1,280 channels, N 16: 512 sequences 23.3 us, 25.8 through the caches; 256
+// sequences 12.8 and 12.2).
 template <typename TI, int N>
 void launch_recurrent_n(const SsmParams& p, unsigned grid, hipStream_t s) {
   const dim3 g(grid), b(256);
-  if (p.rows <= p.B) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1, 1>), g, b, 0, s, p);
-  else if (p.rows <= 4LL * p.B) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1, 4>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 2, 4>), g, b, 0, s, p);
+  const bool stream = (long long)p.B * p.D * p.N * 4 >= 32LL << 20;
+  if (p.rows <= p.B) {
+    if (stream) hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1, 1, true>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1, 1, false>), g, b, 0, s, p);
+  } else if (p.rows <= 4LL * p.B) {
+    hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 1, 4, false>), g, b, 0, s, p);
+  } else {
+    hipLaunchKernelGGL((ssm_recurrent_kernel<TI, N, 2, 4, false>), g, b, 0, s, p);
+  }
 }
 
 template <typename TI>

@@ -275,3 +275,14 @@ def test_gradients_that_start_anywhere():
                               [torch.cat([first, t["dout"]]), torch.cat([torch.zeros_like(states[:1]), t["dhT"]])])
     for a, n in zip(got, ("dx", "dw", "dbias", "dh0")):
         assert torch.equal(a, want[n]), n
+
+
+@pytest.mark.parametrize("first,again", [(0, 1), (0, 64), (63, 255), (0, 256), (255, 256), (300, 599), (511, 512)])
+def test_pool_slots_named_again_far_behind(first, again):
+    """Of two sequences with one slot the first has it, however many lie between."""
+    t, c, pool, slots = pool_case(23, "bf16", 600, 1, 16, 3, 600)
+    slots[again] = slots[first]
+    want_pool, keep = pool.clone(), torch.arange(600, device="cuda") != again
+    want = gdn.conv_fwd_pool(t["x"][keep], t["w"], want_pool, slots[keep], t["bias"])
+    out = gdn.conv_fwd_pool(t["x"], t["w"], pool, slots, t["bias"])
+    assert torch.equal(out[keep], want) and not out[again].any() and torch.equal(pool, want_pool)

@@ -426,3 +426,35 @@ def test_gradients_that_start_anywhere():
     got = torch.autograd.grad([both, hT], leaves, [torch.cat([torch.zeros_like(both[:1]), t["dout"]]), t["dhT"]])
     for v, n in zip(got, ("dx", "ddt", "db", "dc", "dA_log", "dD", "dz", "ddt_bias", "dh0")):
         assert torch.equal(v, want[n]), n
+
+
+@pytest.mark.parametrize("first,again", [(0, 1), (0, 64), (63, 255), (0, 256), (255, 256), (300, 599), (511, 512)])
+def test_pool_slots_named_again_far_behind(first, again):
+    """Of two sequences with one slot the first has it, however many lie between."""
+    t, _ = make(33, "bf16", [1] * 600, 24, 1, 16, False)
+    pool = torch.randn(600, 24, 16, device="cuda")
+    slots = torch.randperm(600, device="cuda").int()
+    slots[again] = slots[first]
+    want_pool, keep = pool.clone(), torch.arange(600, device="cuda") != again
+    a, o = args(t)
+    o = {k: o[k] for k in ("D", "z", "dt_bias")}
+    want = gdn.ssm_fwd_recurrent_pool(*[v[keep] for v in a[:4]], a[4], want_pool, slots[keep], D=o["D"],
+                                      z=o["z"][keep], dt_bias=o["dt_bias"])
+    out = gdn.ssm_fwd_recurrent_pool(*a, pool, slots, **o)
+    assert torch.equal(out[keep], want) and not out[again].any() and torch.equal(pool, want_pool)
+
+
+@pytest.mark.parametrize("N", [16, 64])
+def test_more_states_than_the_caches_hold(N):
+    """The same bits for a batch whose states go past the caches as for its halves."""
+    D = 130 * 1024 // N
+    t, _ = make(34, "bf16", [1] * 72, D, 1, N, False)  # 130 KiB times 4 bytes a sequence
+    pool = torch.randn(80, D, N, device="cuda")
+    slots = torch.randperm(80, device="cuda")[:72].int()
+    halves = pool.clone()
+    a, o = args(t)
+    o = {k: o[k] for k in ("D", "z", "dt_bias")}
+    out = gdn.ssm_fwd_recurrent_pool(*a, pool, slots, **o)
+    parts = [gdn.ssm_fwd_recurrent_pool(*[v[s] for v in a[:4]], a[4], halves, slots[s], D=o["D"], z=o["z"][s],
+                                        dt_bias=o["dt_bias"]) for s in (slice(0, 36), slice(36, 72))]
+    assert torch.equal(out, torch.cat(parts)) and torch.equal(pool, halves)
