@@ -498,7 +498,7 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
 
 // ---------------------------------------------------------------- backwards --
 //
-// Segments of some 25 tokens.  A first launch forms, for sixteen states of a
+// Segments of at most some 25 tokens.  A first launch forms, for sixteen states of a
 // channel, what a segment leaves from zero: the state E going forwards and,
 // going backwards in time, the state's gradient, R = sum_t exp(A (s_1 + .. +
 // s_t)) c_t dy_t, which one forward walk gives too.  The join makes of them the
@@ -609,7 +609,7 @@ template <int N>
 struct Blocks {
   static constexpr int BT = 4, NB = N == 16 ? 6 : 5, BL = BT * NB;
 };
-int segment_rows(int N) { return N == 16 ? Blocks<16>::BL : N == 32 ? Blocks<32>::BL : Blocks<64>::BL; }
+int most_blocks(int N) { return N == 16 ? Blocks<16>::NB : N == 32 ? Blocks<32>::NB : Blocks<64>::NB; }
 
 // a and b become (a's lanes below 32, b's below 32) and (a's from 32 on, b's
 // from 32 on): their sum then holds a's over both halves in the lower lanes
@@ -1001,23 +1001,31 @@ Space space_of(long long segments, long long runs, long long rows, int D, int G,
 
 struct BackPlan {
   long long segments, runs, rows;
-  int nseg, run, waves, teams;
+  int L, nseg, run, waves, teams;
 };
 
 BackPlan back_plan(int B, int T, int D, int G, int N, bool packed) {
   BackPlan b;
   b.rows = (packed ? 1LL : B) * (long long)T;
-  const int L = segment_rows(N), tiles = tiles_of(D / G, 1024 / N);
-  b.nseg = segments_of(T, L);
-  b.segments = B > 0 ? slots_of(packed, B, T, L) : 0;
+  const int tiles = tiles_of(D / G, 1024 / N);
   // Four waves a workgroup, or two where the last one of a group's would
   // otherwise have two to work for nothing.
   b.waves = (tiles + 3) / 4 * 4 - tiles >= 2 ? 2 : 4;
   b.teams = tiles_of(tiles, b.waves);
+  // Segments of as many blocks as there may be, or of so few that all waves still
+  // run at once: where the device is not full, a segment's time is the call's (149
+  // tokens of 561 channels: 12.5 us with two blocks, 31.5 with six; 4 x 487 of 780
+  // 14 and 32).
+  const long long wide = (long long)b.teams * G, places = 2048 / b.waves;
+  for (int blocks = 2;; ++blocks) {
+    b.L = blocks * Blocks<16>::BT;
+    b.segments = B > 0 ? slots_of(packed, B, T, b.L) : 0;
+    if (blocks == most_blocks(N) || b.segments * wide <= places) break;
+  }
+  b.nseg = segments_of(T, b.L);
   // A workgroup takes a run of segments (few partial sums of the parameters'
   // gradients), as long as the device's places (eight waves a compute unit)
   // are in the end filled as well as by shorter ones.
-  const long long wide = (long long)b.teams * G, places = 2048 / b.waves;
   const int first = (int)std::max(1LL, b.segments * wide / (8 * places));
   long long best = 0;
   for (int run = first; run < first + 64; ++run) {
@@ -1050,12 +1058,15 @@ void launch_outputs(const SsmParams& p, unsigned grid, bool output, hipStream_t 
 }
 
 // Few states of many segments take eight threads each (20,480 states of 200
-// segments: 16 us instead of 25); many keep the device busy with one (245,760
-// states of some 13 segments: 14 us instead of 51).
+// segments: 16 us instead of 25) or 32 (1,056 of 730: 8 instead of 19; but 6,400
+// of 485 25 instead of 15, in pieces of 32 bytes); many states keep the device busy
+// with one (245,760 of some 13 segments: 14 us, 51 with eight).
 void launch_join(const SsmParams& p, long long states, int directions, hipStream_t s) {
-  const int groups = p.segments / p.B > 64 && states < 65536 ? 8 : 1;
+  const long long each = p.segments / p.B;
+  const int groups = states < 65536 && each > 64 ? states < 4096 && each > 256 ? 32 : 8 : 1;
   const dim3 grid((unsigned)std::min(MOST_WGS, (states * groups + 255) / 256), directions);
-  if (groups > 1) hipLaunchKernelGGL((ssm_join_kernel<8>), grid, dim3(256), 0, s, p);
+  if (groups == 32) hipLaunchKernelGGL((ssm_join_kernel<32>), grid, dim3(256), 0, s, p);
+  else if (groups == 8) hipLaunchKernelGGL((ssm_join_kernel<8>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((ssm_join_kernel<1>), grid, dim3(256), 0, s, p);
 }
 
@@ -1223,7 +1234,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
   p.keys = reinterpret_cast<float*>(base + w.keys);
   p.sums = reinterpret_cast<float*>(base + w.sums);
   p.B = B; p.T = T; p.D = D; p.G = G; p.N = N; p.Dg = D / G;
-  p.L = segment_rows(N);
+  p.L = plan.L;
   p.nseg = plan.nseg;
   p.segments = plan.segments;
   p.run = plan.run;

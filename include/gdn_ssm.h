@@ -127,9 +127,9 @@ long long gdn_ssm_workspace_size(int B, int T, int D, int G, int N, int packed,
  * dh0 may be dhT itself.  The parameters' gradients are written for B == 0 and
  * T == 0 too (zeros).  Rows of no sequence are left as they were.  Sums over
  * tokens and channels are taken in fp32 in a fixed order.  Everything else is
- * gdn_ssm_fwd's; sequences are always cut, into segments of 20 or 24 tokens. Where a
- * state or its gradient is not finite, the parameters' gradients of its channel
- * may be NaN.
+ * gdn_ssm_fwd's; sequences are always cut, into segments of 8 to 24 tokens.
+ * Where a state or its gradient is not finite, the parameters' gradients of its
+ * channel may be NaN.
  */
 int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const void* c,
                 const float* A_log, const float* Dskip, const void* z,

@@ -458,3 +458,18 @@ def test_more_states_than_the_caches_hold(N):
     parts = [gdn.ssm_fwd_recurrent_pool(*[v[s] for v in a[:4]], a[4], halves, slots[s], D=o["D"], z=o["z"][s],
                                         dt_bias=o["dt_bias"]) for s in (slice(0, 36), slice(36, 72))]
     assert torch.equal(out, torch.cat(parts)) and torch.equal(pool, halves)
+
+
+@pytest.mark.parametrize("N,D", [(16, 300), (32, 150), (64, 75)])
+@pytest.mark.parametrize("B", [40, 60, 80, 110, 120])
+def test_backward_segments_of_every_length(N, D, B):
+    """More sequences take longer segments, of two blocks of tokens up to all there may be."""
+    t, c = make(B, "bf16", [50] * B, D, 1, N, False)
+    check_backward(t, c, "bf16")
+
+
+@pytest.mark.parametrize("D", [16, 33])
+def test_few_states_of_many_segments(D):
+    t, c = make(35, "f32", [6100, 5], D, 1, 16, True)
+    check_forward(t, c, "f32")
+    check_backward(t, c, "f32")
