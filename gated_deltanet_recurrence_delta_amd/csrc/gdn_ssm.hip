@@ -957,22 +957,31 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   Cut c = {false, std::max(T, 1), 1, 0};
   if (B == 0) return c;
   const long long tiles = (long long)G * tiles_of(D / G, 64), chains = B * tiles;
-  // Three launches and a lane a channel against one launch and N / 4 lanes: with
-  // 256 channels the same at some 160 tokens for N 16 and 360 for N 64.
-  if (T <= 96 + 4 * N) {
+  // Enough waves without a cut: one launch, a lane a channel, and a second reading
+  // saved (60 x 1,280 channels, N 16: 256 tokens 124 us, 158 cut in three; at 48
+  // sequences 94 and 122, but N 32 224 and 228, and 1,043 and 774 for 1,024 tokens).
+  const bool uncut = !packed && chains > WAVES / 4;
+  // Token by token, N / 4 lanes a channel in one launch: as long as that takes less
+  // than the cut's three (N 16: 20 us against 17 for 128 tokens of few channels,
+  // 38 and 41 for 256 of 8 x 1,280; N 64: 29 and 32 for 192 of few, 169 and 204 for
+  // 512 of 8 x 1,280), or where sequences are not cut for the shortest (400 x 1,280,
+  // N 16: 25 us against 18 for 4 tokens; 60 and more the same).
+  if (T <= (uncut ? 4 : 64 + 2 * N + std::min(chains, 160LL) * N / 16)) {
     c.recurrent = true;
     return c;
   }
-  if (!packed && chains > WAVES / 3) return c;
+  if (uncut) return c;
   const long long rows = packed ? T : (long long)B * T;
-  // rows over the segments that there may be; of packed sequences the last
-  // segments are short
-  const long long segments = std::max(1LL, packed ? WAVES / tiles - B / 2 : WAVES / chains * B);
-  long long L = (rows + segments - 1) / segments;
-  if (!packed) L = (T + segments / B - 1) / (segments / B);
-  // (2 x 2,013 x 96, N 64: 64 us with 20 rows at least, 86 with 32, 66 with 12; 4
-  // x 1,000 x 512, N 16: 42, 40, 44)
-  c.L = (int)std::max(20LL, (L + FLIGHT - 1) / FLIGHT * FLIGHT);
+  // Rows a segment for so many waves; of packed sequences the last segments are short.
+  auto length = [&](long long waves) {
+    const long long segments = std::max(1LL, packed ? waves / tiles - B / 2 : waves / chains * B), each = segments / std::max(B, 1);
+    const long long L = packed ? (rows + segments - 1) / segments : (T + each - 1) / each;
+    return (L + FLIGHT - 1) / FLIGHT * FLIGHT;
+  };
+  // Half as many waves before segments go below 20 rows, and no fewer than 8 (2 x
+  // 2,013 x 96, N 64: 57 us with 8, 71 with 20; 1,000 x 128, N 16: 20 and 28; 8,192
+  // x 256: 42 with the 16 of half the waves, 53 with 8, 43 with 20).
+  c.L = (int)std::max(length(WAVES), std::min(20LL, std::max(8LL, length(WAVES / 2))));
   if (c.L >= T) {
     c.L = T;
     return c;

@@ -473,3 +473,18 @@ def test_few_states_of_many_segments(D):
     t, c = make(35, "f32", [6100, 5], D, 1, 16, True)
     check_forward(t, c, "f32")
     check_backward(t, c, "f32")
+
+
+@pytest.mark.parametrize("N", [16, 32, 64])
+@pytest.mark.parametrize("T", [4, 5, 6, 31])
+def test_many_sequences_of_few_tokens(N, T):
+    """More waves than the device needs: a lane a channel from five tokens on, no cut."""
+    assert gdn.gdn_ssm_workspace_size(1100, T, 8, 1, N, 0, 1) == 0
+    check_forward(*make(N + T, "bf16", [T] * 1100, 8, 1, N, False), "bf16")
+
+
+@pytest.mark.parametrize("N", [16, 32, 64])
+def test_packed_sequences_cut(N):
+    lens = [433, 1, 0, 7, 20, 8, 431]
+    assert gdn.gdn_ssm_workspace_size(len(lens), sum(lens), 40, 1, N, 1, 1) > 0
+    check_forward(*make(N, "bf16", lens, 40, 1, N, True), "bf16")
