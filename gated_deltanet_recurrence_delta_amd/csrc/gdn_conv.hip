@@ -165,8 +165,9 @@ __device__ static inline void window_at(Vals<V> (&window)[W - 1], Channels<TI, V
   }
 }
 
-// Rows on their way at once (the backward pass of 4 x 4,096 x 1,280 bf16: 37 us
-// a call, 39 with two, 45 with eight).
+// Rows on their way at once (4 x 4,096 x 1,280 bf16: forwards 17.8 us a call and
+// backwards 32.6; 18.1 and 32.5 with two, 18.4 and 37.1 with eight; 4 x 2,048 x
+// 1,024 fp32 forwards 12.8, 13.3 and 13.9).
 constexpr int FLIGHT = 4;
 
 // A wave's unit: a segment (uniform, and the compiler is told so) and a tile.
@@ -267,8 +268,8 @@ __global__ __launch_bounds__(64 * WAVES) void conv_bwd_kernel(const ConvParams p
         gn[f] = ch.load(dout + (long)f * D);
       }
     for (int t = 0; t < rows; t += FLIGHT) {
-      // (all of a turn's loads at its beginning: 37 us a call, 43 where each row's
-      // follows the row before)
+      // (all of a turn's loads at its beginning: a seventh more a call where each
+      // row's follows the row before)
       typename Channels<TI, V, NEXT>::raw xr[FLIGHT], gr[FLIGHT];
 #pragma unroll
       for (int f = 0; f < FLIGHT; ++f) {
@@ -382,8 +383,8 @@ __global__ __launch_bounds__(1024) void conv_weights_kernel(const float* part, i
 
 // Rows a segment: 32 (each reads up to 2 (W - 1) rows more of what its
 // neighbours read), fewer where that leaves less than some three waves for each
-// vector unit.  Whole forward calls: 8 x 4,096 x 1,280 bf16 40 us with 32 rows,
-// 43 with 16; 4 x 4,096 21 with 16, 25 with 8; 4 x 2,048 x 1,024 fp32 13 with 8,
+// vector unit.  Whole forward calls: 8 x 4,096 x 1,280 bf16 34 us with 32 rows,
+// 40 with 16; 4 x 4,096 18 with 16, 21 with 32; 4 x 2,048 x 1,024 fp32 13 with 8,
 // 18 with 16.
 int rows_a_segment(long long rows, int D, int V, bool back) {
   int L = 32;
@@ -394,7 +395,7 @@ int rows_a_segment(long long rows, int D, int V, bool back) {
 
 // Channels a lane: 16 bytes of neighbours forwards, 8 bytes of bf16 backwards
 // (two windows and the sums in registers) where every row starts aligned to
-// them, else four, 64 apart (6 x 32,530 rows of 271 channels, W 3: 82 us forwards
+// them, else four, 64 apart (6 x 32,530 rows of 271 channels, W 3: 75 us forwards
 // and 120 backwards, 112 and 174 with one channel a lane), or one where there are
 // not more than a wave's.
 struct Width {

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormParams p) {
   constexpr int GROUPS = NT / LR;
   // Rows of one token in flight at once; backwards, with three vectors a row, two
   // leave more waves (4 x 4,096 tokens, 16 + 4 heads of 128, neighbours paired:
-  // 61 us a call, 67 with four).
+  // 58 us a call, 67 with four).
   constexpr int FLIGHT = BACK ? 2 : 4;
   const int side = (int)blockIdx.x < p.wgs[0] ? 0 : 1;
   const int wg = blockIdx.x - (side ? p.wgs[0] : 0), nwg = p.wgs[side];

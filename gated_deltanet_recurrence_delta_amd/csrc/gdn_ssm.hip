@@ -179,6 +179,11 @@ struct KeyPair {
 // sequences are cut, else h0).  Otherwise the state that a segment leaves from
 // zero, and the sum of its steps; what follows the last segment is hT, which
 // the outputs' launch gives.
+//
+// Bound by the vector unit's instructions: a state's update takes 27.5 cycles of it
+// (a multiplication for the exponent, the exponential's 9.7, a product, two fused
+// ones).  8 x 4,096 tokens of 1,280 channels, N 16: 149 us the outputs, 115 the
+// states before, with four waves a unit.
 template <typename TI, int N, bool OUTPUT>
 __global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
   const Place w = place_of(p);
@@ -597,14 +602,18 @@ __global__ __launch_bounds__(256) void ssm_bwd_maps_kernel(const SsmParams p) {
 // 4 i + j also owns channel j of its group for what is the channel's alone: the
 // step, the gate, the stores.  Those values go to the other lanes by DPP.
 //
-// A segment is NB blocks of BT tokens.  A walk forwards keeps the states at the
-// blocks' starts; then, from the last block on, a block's states are formed
+// A segment is at most NB blocks of BT tokens.  A walk forwards keeps the states
+// at the blocks' starts; then, from the last block on, a block's states are formed
 // again and kept in registers, and its tokens are taken backwards.
+//
+// Bound by the vector unit's instructions, three exponentials a state's update
+// among them (5,003 rows of 640 channels, N 32: 143 us, the maps 52, against 75 for
+// both passes forwards).
 
 // More tokens a block need more registers, more blocks more LDS (a workgroup of
 // four waves has 80 KB of it and 256 registers, so that two share a compute
 // unit), and shorter segments more joining (4 x 4,096 x 1,280, N 16, whole
-// calls: 4 x 6 505 us, 4 x 5 542, 5 x 6 522, 6 x 5 541, 8 x 4 560).
+// calls: 4 x 6 513 us, 4 x 5 542, 5 x 6 522, 6 x 5 541, 8 x 4 560).
 template <int N>
 struct Blocks {
   static constexpr int BT = 4, NB = N == 16 ? 6 : 5, BL = BT * NB;
@@ -886,26 +895,29 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmParams 
   }
 }
 
-// db and dc of the workgroups' sums, where a group's channels are several
-// workgroups'.  Rows of no sequence are left as they were.
+// What the workgroups' sums leave to do, in one launch: the parameters' gradients,
+// 64 of them a workgroup, 16 threads each; and behind those workgroups, where a
+// group's channels are several workgroups', db and dc.  Rows of no sequence are
+// left as they were.
 template <typename TI>
-__global__ __launch_bounds__(256) void ssm_keys_kernel(const SsmParams p, int teams) {
-  const long GN = (long)p.G * p.N, total = p.rows * GN * 2;
-  for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long)gridDim.x * 256) {
-    const int n = (int)(e % p.N), which = (int)(e / p.N % 2);
-    const long rg = e / (2 * p.N), row = rg / p.G;
-    if (p.cu && (row < p.cu[0] || row >= p.cu[p.B])) continue;
-    float a = 0.f;
-    for (int q = 0; q < teams; ++q) a += p.keys[(long)q * total + e];
-    static_cast<TI*>(which ? p.dc : p.db)[rg * p.N + n] = (TI)a;
-  }
-}
-
-// The parameters' gradients: 64 of them a workgroup, 16 threads each.
-__global__ __launch_bounds__(1024) void ssm_sums_kernel(const SsmParams p) {
+__global__ __launch_bounds__(1024) void ssm_sums_kernel(const SsmParams p, int teams) {
   __shared__ float sums[16][64];
+  const long DN = (long)p.D * p.N, cols = DN + 2L * p.D;
+  const int own = (int)((cols + 63) / 64);
+  if ((int)blockIdx.x >= own) {
+    const long GN = (long)p.G * p.N, total = p.rows * GN * 2;
+    for (long e = (long)(blockIdx.x - own) * 1024 + threadIdx.x; e < total; e += (long)(gridDim.x - own) * 1024) {
+      const int n = (int)(e % p.N), which = (int)(e / p.N % 2);
+      const long rg = e / (2 * p.N), row = rg / p.G;
+      if (p.cu && (row < p.cu[0] || row >= p.cu[p.B])) continue;
+      float a = 0.f;
+      for (int q = 0; q < teams; ++q) a += p.keys[(long)q * total + e];
+      static_cast<TI*>(which ? p.dc : p.db)[rg * p.N + n] = (TI)a;
+    }
+    return;
+  }
   const int lane = threadIdx.x & 63, k = threadIdx.x >> 6;
-  const long DN = (long)p.D * p.N, cols = DN + 2L * p.D, c = (long)blockIdx.x * 64 + lane;
+  const long c = (long)blockIdx.x * 64 + lane;
   float a = 0.f;
   if (c < cols)
 #pragma unroll 4
@@ -1261,13 +1273,11 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
     else hipLaunchKernelGGL((ssm_bwd_maps_kernel<float>), dim3((unsigned)maps), dim3(256), 0, s, p);
     launch_join(p, (long long)B * D * N, 2, s);
     bf ? launch_bwd<__bf16>(p, plan.waves, (unsigned)wgs, s) : launch_bwd<float>(p, plan.waves, (unsigned)wgs, s);
-    if (plan.teams > 1 && plan.rows > 0) {
-      const long long total = plan.rows * G * 2 * N;
-      const unsigned grid = (unsigned)std::min<long long>(4096, (total + 255) / 256);
-      if (bf) hipLaunchKernelGGL((ssm_keys_kernel<__bf16>), dim3(grid), dim3(256), 0, s, p, plan.teams);
-      else hipLaunchKernelGGL((ssm_keys_kernel<float>), dim3(grid), dim3(256), 0, s, p, plan.teams);
-    }
   }
-  hipLaunchKernelGGL(ssm_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, p);
+  // (the first workgroups the parameters' gradients', at most 4,096 more for db and dc)
+  const long long keyed = plan.segments > 0 && plan.teams > 1 ? plan.rows * G * 2 * N : 0;
+  const dim3 grid((unsigned)((cols + 63) / 64 + std::min(4096LL, (keyed + 1023) / 1024)));
+  if (bf) hipLaunchKernelGGL((ssm_sums_kernel<__bf16>), grid, dim3(1024), 0, s, p, plan.teams);
+  else hipLaunchKernelGGL((ssm_sums_kernel<float>), grid, dim3(1024), 0, s, p, plan.teams);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
