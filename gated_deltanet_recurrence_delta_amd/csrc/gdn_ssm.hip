@@ -182,8 +182,8 @@ struct KeyPair {
 //
 // Bound by the vector unit's instructions: a state's update takes 27.5 cycles of it
 // (a multiplication for the exponent, the exponential's 9.7, a product, two fused
-// ones).  8 x 4,096 tokens of 1,280 channels, N 16: 149 us the outputs, 115 the
-// states before, with four waves a unit.
+// ones).  8 x 4,096 tokens of 1,280 channels, N 16: 254 us, 42% of it the states that
+// segments leave and 5% the join; 117 would be one pass's updates.
 template <typename TI, int N, bool OUTPUT>
 __global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
   const Place w = place_of(p);
@@ -961,9 +961,11 @@ struct Cut {
   bool cut() const { return segments > 0; }
 };
 
-// Waves that keep the device's 1,024 vector units busy, four on each: no more,
-// or some units get a fifth and the others wait for it.
-constexpr long long WAVES = 4096;
+// The waves that the device's 1,024 vector units hold at once, by the states that a
+// lane keeps in registers: no more, or some units get another and the rest wait for
+// it (8 x 4,096 x 1,280, N 16: 255 us, 265 with 4,096 and 268 with 8,192; 4 x 4,096,
+// N 32: 283, 285 with 5,120; 2 x 4,096, N 64: 299, 331 with 4,096).
+long long most_waves(int N) { return N == 16 ? 5120 : N == 32 ? 4096 : 2048; }
 
 Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   Cut c = {false, std::max(T, 1), 1, 0};
@@ -972,7 +974,7 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   // Enough waves without a cut: one launch, a lane a channel, and a second reading
   // saved (60 x 1,280 channels, N 16: 256 tokens 124 us, 158 cut in three; at 48
   // sequences 94 and 122, but N 32 224 and 228, and 1,043 and 774 for 1,024 tokens).
-  const bool uncut = !packed && chains > WAVES / 4;
+  const bool uncut = !packed && chains > 1024;
   // Token by token, N / 4 lanes a channel in one launch: as long as that takes less
   // than the cut's three (N 16: 20 us against 17 for 128 tokens of few channels,
   // 38 and 41 for 256 of 8 x 1,280; N 64: 29 and 32 for 192 of few, 169 and 204 for
@@ -990,10 +992,10 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
     const long long L = packed ? (rows + segments - 1) / segments : (T + each - 1) / each;
     return (L + FLIGHT - 1) / FLIGHT * FLIGHT;
   };
-  // Half as many waves before segments go below 20 rows, and no fewer than 8 (2 x
-  // 2,013 x 96, N 64: 57 us with 8, 71 with 20; 1,000 x 128, N 16: 20 and 28; 8,192
-  // x 256: 42 with the 16 of half the waves, 53 with 8, 43 with 20).
-  c.L = (int)std::max(length(WAVES), std::min(20LL, std::max(8LL, length(WAVES / 2))));
+  // No more than 2,048 waves where segments go below 20 rows, and no fewer rows than
+  // 8 (2 x 2,013 x 96, N 64: 57 us with 8, 71 with 20; 1,000 x 128, N 16: 20 and 28;
+  // 8,192 x 256: 42 with the 16 of 2,048 waves, 53 with 8, 43 with 20).
+  c.L = (int)std::max(length(most_waves(N)), std::min(20LL, std::max(8LL, length(2048))));
   if (c.L >= T) {
     c.L = T;
     return c;
