@@ -189,3 +189,38 @@ def test_a_captured_training_step_of_a_layer():
         assert torch.equal(o, out) and all(torch.equal(g[n], h[n]) for n in g if g[n] is not None)
         assert all(torch.equal(gc[n], hc[n]) for n in gc)
     assert eager.requires_grad
+
+
+def test_two_calls_at_once():
+    """The operators on two streams side by side give the bits they give alone."""
+    def work(seed):
+        B, T, D, N, H, d = 2, 700, 192, 16, 3, 64
+        p = {k: v.detach() for k, v in scan_layer(seed, B, T, D, N, torch.bfloat16).items()}
+        a = torch.arange(T)[:, None] * 100.0 ** (-torch.arange(0, 16, 2) / 16)
+        cos, sin = torch.cos(a).cuda(), torch.sin(a).cuda()
+        q, k, w = rand(seed + 20, B, T, H, d), rand(seed + 21, B, T, H, d), 1 + rand(seed + 22, d, scale=0.1)
+        dout = rand(seed + 23, B, T, D, dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+
+        def run():
+            y, tail = gdn.conv_fwd(p["x"], p["w"], p["bias"])
+            scan = (y, p["dt"], p["b"], p["c"], p["A_log"])
+            out, hT = gdn.ssm_fwd(*scan, p["D"], p["z"], p["dt_bias"])
+            g = gdn.ssm_bwd(*scan, dout, D=p["D"], z=p["z"], dt_bias=p["dt_bias"], dhT=hT)
+            h = gdn.conv_bwd(p["x"], p["w"], g["dx"], p["bias"], dhT=tail)
+            n = gdn.qk_norm_bwd(q, k, q, k, cos, sin, wq=w, wk=w)
+            return [y, tail, out, hT, *g.values(), *h.values(), *n.values()]
+        return run
+
+    runs = [work(70), work(90)]
+    alone = [run() for run in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        got = []
+        for run, stream in zip(runs, streams):
+            with torch.cuda.stream(stream):
+                got.append(run())
+        torch.cuda.synchronize()
+        for one, other in zip(got, alone):
+            assert all(torch.equal(u, v) for u, v in zip(one, other))
