@@ -797,7 +797,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmParams 
             for (int j = 0; j < 4; ++j) y[c] = __builtin_fmaf(c4[j], h[c][j], y[c]);
           }
           const float yo = __builtin_fmaf(skip, x, sum_own<LC>(y, odd, high));
-          Row<TI>::store_inside(static_cast<TI*>(p.dz) + at + (long)t * D, i < cnt && p.dz ? D * (int)sizeof(TI) : 0, mine_at,
+          Row<TI>::store_inside(static_cast<TI*>(p.dz) + at + (long)t * D,
+                                i < cnt && p.dz ? D * (int)sizeof(TI) : 0, mine_at,
                                 dy * yo * (q * __builtin_fmaf(z, 1.f - q, 1.f)));
         }
         dyo[i] = GATE ? dy * z * q : dy;
@@ -978,9 +979,10 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   // Token by token, N / 4 lanes a channel in one launch: as long as that takes less
   // than the cut's three (N 16: 20 us against 17 for 128 tokens of few channels,
   // 38 and 41 for 256 of 8 x 1,280; N 64: 29 and 32 for 192 of few, 169 and 204 for
-  // 512 of 8 x 1,280), or where sequences are not cut for the shortest (400 x 1,280,
-  // N 16: 25 us against 18 for 4 tokens; 60 and more the same).
-  if (T <= (uncut ? 4 : 64 + 2 * N + std::min(chains, 160LL) * N / 16)) {
+  // 512 of 8 x 1,280); where sequences are not cut, for single tokens (160 x 1,280,
+  // N 32: 13 us against 18, for two tokens 20 and 19; of 400 sequences 31 and 34, 45
+  // and 33; N 64 of 60 sequences 11 and 19, 15 and 19).
+  if (T <= (uncut ? 1 : 64 + 2 * N + std::min(chains, 160LL) * N / 16)) {
     c.recurrent = true;
     return c;
   }
@@ -988,7 +990,8 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   const long long rows = packed ? T : (long long)B * T;
   // Rows a segment for so many waves; of packed sequences the last segments are short.
   auto length = [&](long long waves) {
-    const long long segments = std::max(1LL, packed ? waves / tiles - B / 2 : waves / chains * B), each = segments / std::max(B, 1);
+    const long long segments = std::max(1LL, packed ? waves / tiles - B / 2 : waves / chains * B);
+    const long long each = segments / std::max(B, 1);  // of a dense sequence: one at least
     const long long L = packed ? (rows + segments - 1) / segments : (T + each - 1) / each;
     return (L + FLIGHT - 1) / FLIGHT * FLIGHT;
   };
@@ -1276,7 +1279,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
     launch_join(p, (long long)B * D * N, 2, s);
     bf ? launch_bwd<__bf16>(p, plan.waves, (unsigned)wgs, s) : launch_bwd<float>(p, plan.waves, (unsigned)wgs, s);
   }
-  // (the first workgroups the parameters' gradients', at most 4,096 more for db and dc)
+  // (a workgroup for 64 of the parameters' gradients, at most 4,096 more for db and dc)
   const long long keyed = plan.segments > 0 && plan.teams > 1 ? plan.rows * G * 2 * N : 0;
   const dim3 grid((unsigned)((cols + 63) / 64 + std::min(4096LL, (keyed + 1023) / 1024)));
   if (bf) hipLaunchKernelGGL((ssm_sums_kernel<__bf16>), grid, dim3(1024), 0, s, p, plan.teams);

@@ -488,3 +488,8 @@ def test_packed_sequences_cut(N):
     lens = [433, 1, 0, 7, 20, 8, 431]
     assert gdn.gdn_ssm_workspace_size(len(lens), sum(lens), 40, 1, N, 1, 1) > 0
     check_forward(*make(N, "bf16", lens, 40, 1, N, True), "bf16")
+
+
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_many_sequences_of_one_to_three_tokens(T):
+    check_forward(*make(T, "f32", [T] * 1030, 9, 3, 16, False), "f32")
