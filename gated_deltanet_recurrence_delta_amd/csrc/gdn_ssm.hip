@@ -93,6 +93,14 @@ __device__ static inline float rate_of(float A_log) {
   return a < -3e38f ? -3e38f : a;
 }
 
+// exp(A_log) as the factor of a gradient, a finite number likewise: where the
+// sum over the tokens is zero, as it is for a state that keeps nothing, so is the
+// product.
+__device__ static inline float rate_factor(float A_log) {
+  const float a = expf(A_log);
+  return a > 3e38f ? 3e38f : a;
+}
+
 // -------------------------------------------------------------------- keys --
 
 // Sixteen values of a token's key through the scalar unit: the address is the
@@ -927,7 +935,7 @@ __global__ __launch_bounds__(1024) void ssm_sums_kernel(const SsmParams p, int t
   __syncthreads();
   if (k == 0 && c < cols) {
     for (int i = 1; i < 16; ++i) a += sums[i][lane];
-    if (c < DN) p.dA_log[c] = -expf(p.A_log[c]) * a;
+    if (c < DN) p.dA_log[c] = -rate_factor(p.A_log[c]) * a;
     else if (c < DN + p.D) {
       if (p.dD) p.dD[c - DN] = a;
     } else if (p.ddt_bias) {

@@ -493,3 +493,14 @@ def test_packed_sequences_cut(N):
 @pytest.mark.parametrize("T", [1, 2, 3])
 def test_many_sequences_of_one_to_three_tokens(T):
     check_forward(*make(T, "f32", [T] * 1030, 9, 3, 16, False), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [0, 1, 70, 402])
+def test_gradients_of_rates_beyond_the_numbers(dtype, T):
+    """A state that keeps nothing has no say in its rate: exp(s A) = 0 makes every term of the gradient zero."""
+    t, c = make(36, dtype, [T], 20, 1, 16, True)
+    t["A_log"][:, 0], t["A_log"][3, 5], t["A_log"][:, 1] = 100.0, 89.0, float("inf")
+    g = backward(t)["dA_log"]
+    assert g.isfinite().all()
+    assert not g[:, :2].any() and not g[3, 5].any() and g[:3, 2:].any() == (T > 0)
