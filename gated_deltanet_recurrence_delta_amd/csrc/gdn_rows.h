@@ -164,15 +164,17 @@ inline long long slots_of(bool packed, long long B, long long T, long long L) {
 
 __device__ static inline int taken(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
-// How many sequences begin at or before the slot: a search that looks at 64
-// offsets at once.  All 64 lanes take part, with one slot.
-__device__ static inline int sequences_before(const int32_t* cu, int B, int T, int L, long slot) {
+// How many of the first numbers below B a condition holds for, which holds for none
+// behind the first that it fails for: a search that looks at 64 of them at once.
+// All 64 lanes take part, with one condition.
+template <typename F>
+__device__ static inline int leading(int B, F holds) {
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = B;
   while (lo < hi) {
     const int step = (hi - lo + 63) >> 6;
     const long at = lo + (long)lane * step;
-    const bool before = at < hi && taken(cu[at < hi ? at : lo], 0, T) / L + at <= slot;
+    const bool before = at < hi && holds((int)(at < hi ? at : lo));
     const int c = __popcll(__ballot(before));
     if (step == 1) return lo + c;
     if (c == 0) return lo;
@@ -186,7 +188,7 @@ __device__ static inline Segment segment_of(const int32_t* cu, int B, int T, int
   Segment s;
   int i;
   if (cu) {
-    s.n = sequences_before(cu, B, T, L, slot) - 1;
+    s.n = leading(B, [&](int n) { return taken(cu[n], 0, T) / L + (long)n <= slot; }) - 1;
     if (s.n < 0) return Segment{0, -1, 0, 0, 0};
     const int b = taken(cu[s.n], 0, T), e = taken(cu[s.n + 1], b, T);
     s.total = e - b;
@@ -204,6 +206,33 @@ __device__ static inline Segment segment_of(const int32_t* cu, int B, int T, int
   s.row0 += t0;
   s.len = min(L, s.total - s.t0);
   return s;
+}
+
+// The last sequence that begins at or before a row, -1: none.
+__device__ static inline int sequence_at(const int32_t* cu, int B, int T, int row) {
+  return leading(B, [&](int n) { return taken(cu[n], 0, T) <= row; }) - 1;
+}
+
+// Of a packed batch the k-th segment that is not its sequence's last: each holds
+// one row whose number is a multiple of L, so that there are rows / L at most,
+// however many sequences there are; n = -1 where row k L is in none.
+__device__ static inline Segment inner_segment_of(const int32_t* cu, int B, int T, int L, int k, long& slot) {
+  const int row = (int)min((long)k * L, (long)T);
+  const int n = sequence_at(cu, B, T, row);
+  if (n < 0) return Segment{0, -1, 0, 0, 0};
+  const int b = taken(cu[n], 0, T), total = taken(cu[n + 1], b, T) - b;
+  const int i = (row - b) / L, t0 = i * L;
+  if (row < b || L >= total - t0) return Segment{0, -1, 0, 0, 0};
+  slot = b / L + n + (long)i;
+  return Segment{(long)b + t0, n, t0, L, total};
+}
+
+// The last segment of sequence n of a packed batch.
+__device__ static inline Segment last_segment_of(const int32_t* cu, int T, int L, int n, long& slot) {
+  const int b = taken(cu[n], 0, T), total = taken(cu[n + 1], b, T) - b;
+  const int i = max(total - 1, 0) / L, t0 = i * L;
+  slot = b / L + n + (long)i;
+  return Segment{(long)b + t0, n, t0, total - t0, total};
 }
 
 // A whole sequence as one segment; any offsets.

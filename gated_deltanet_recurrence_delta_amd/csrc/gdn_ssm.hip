@@ -59,6 +59,8 @@ struct SsmParams {
   int B, T, D, G, N, Dg, nslots;
   int L, nseg;   // rows a segment, segments a dense sequence
   long segments;
+  int inner;     // forwards, packed: so many places for segments that are not their sequence's last, by the rows L apart
+                 // (inner_segment_of); 0: segments are found by their slots
   int run, runs; // backwards: segments a workgroup, and workgroups' runs
   long rows;
   int softplus;
@@ -139,6 +141,7 @@ struct Place {
 
 // A workgroup is one wave: no wave waits for another, and any number of tiles is
 // spread evenly.
+template <bool LAST>
 __device__ static inline Place place_of(const SsmParams& p) {
   const int lane = threadIdx.x & 63, tiles = (p.Dg + 63) >> 6;
   Place w;
@@ -147,7 +150,14 @@ __device__ static inline Place place_of(const SsmParams& p) {
   k /= tiles;
   w.g = k % p.G;
   w.slot = k / p.G;
-  w.s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, w.slot);
+  if (!p.inner) {
+    w.s = segment_of(p.cu, p.B, p.T, p.L, p.nseg, w.slot);
+  } else {
+    // the sequences' last segments, then (alone where LAST is false) the others
+    const int u = (int)w.slot, first = LAST ? p.B : 0;
+    if (u < first) w.s = last_segment_of(p.cu, p.T, p.L, u, w.slot);
+    else w.s = inner_segment_of(p.cu, p.B, p.T, p.L, u - first, w.slot);
+  }
   w.active = c < p.Dg;
   w.d = w.g * p.Dg + min(c, p.Dg - 1);
   return w;
@@ -184,7 +194,7 @@ struct KeyPair {
 };
 
 // Forwards.  OUTPUT: the outputs from the segment's start state (E if the
-// sequences are cut, else h0).  Otherwise the state that a segment leaves from
+// sequence is cut, else h0).  Otherwise the state that a segment leaves from
 // zero, and the sum of its steps; what follows the last segment is hT, which
 // the outputs' launch gives.
 //
@@ -194,7 +204,7 @@ struct KeyPair {
 // segments leave and 5% the join; 117 would be one pass's updates.
 template <typename TI, int N, bool OUTPUT>
 __global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
-  const Place w = place_of(p);
+  const Place w = place_of<OUTPUT>(p);
   if (w.s.n < 0 || (!OUTPUT && w.s.last()) || !w.active) return;
   const int D = p.D, d = w.d;
   Vals<N> A, h;
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(64) void ssm_kernel(const SsmParams p) {
     h[i] = 0.f;
   }
   if constexpr (OUTPUT) {
-    if (p.E) load_states<N>(h, p.E + (w.slot * D + d) * N);
+    if (p.E && !(w.s.first() && w.s.last())) load_states<N>(h, p.E + (w.slot * D + d) * N);
     else if (p.h0) load_states<N>(h, p.h0 + ((long)w.s.n * D + d) * N);
   }
   const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = OUTPUT && p.Dskip ? p.Dskip[d] : 0.f;
@@ -300,8 +310,18 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
   const long DN = (long)p.D * p.N;
   const int lane = threadIdx.x % STATES, group = threadIdx.x / STATES;
   const bool back = blockIdx.y;
-  for (long id0 = (long)blockIdx.x * STATES; id0 < p.B * DN; id0 += (long)gridDim.x * STATES) {
-    const long id = min(id0 + lane, p.B * DN - 1);
+  long from = (long)blockIdx.x * STATES, to = p.B * DN, stride = (long)gridDim.x * STATES;
+  if (p.inner) {  // some workgroups for each row k L, and work where it is the first such row of a cut sequence
+    const int parts = gridDim.x / p.inner, row = (int)(blockIdx.x / parts) * p.L, n = sequence_at(p.cu, p.B, p.T, row);
+    if (n < 0) return;
+    const int b = taken(p.cu[n], 0, p.T), e = taken(p.cu[n + 1], b, p.T);
+    if (row < b || row - b >= p.L || e - b <= p.L) return;
+    from = n * DN + (long)(blockIdx.x % parts) * STATES;
+    to = (n + 1) * DN;
+    stride = (long)parts * STATES;
+  }
+  for (long id0 = from; id0 < to; id0 += stride) {
+    const long id = min(id0 + lane, to - 1);
     const int n = (int)(id / DN);
     const long r = id - n * DN;
     const int d = (int)(r / p.N);
@@ -347,7 +367,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
     h = begun;
     if constexpr (GROUPS > 1)
       for (int g = 0; g < group; ++g) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * sums[g][lane]), h, ends[g][lane]);
-    if (id0 + lane >= p.B * DN) continue;
+    if (id0 + lane >= to) continue;
     for (int i = i0; i < i1; i += F) {
       load(i);
 #pragma unroll
@@ -359,11 +379,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmParams p) {
         }
     }
     if (group != GROUPS - 1) continue;
-    if (back) {
-      if (p.dh0) p.dh0[id] = h;
-    } else if (count == 0) {
-      p.E[slot * DN + r] = h;  // an empty sequence's one segment
-    }
+    if (back && p.dh0) p.dh0[id] = h;
   }
 }
 
@@ -967,6 +983,7 @@ struct Cut {
   bool recurrent;  // token by token, lanes across the states
   int L, nseg;
   long long segments;
+  int inner;      // see SsmParams
   bool cut() const { return segments > 0; }
 };
 
@@ -977,7 +994,7 @@ struct Cut {
 long long most_waves(int N) { return N == 16 ? 5120 : N == 32 ? 4096 : 2048; }
 
 Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
-  Cut c = {false, std::max(T, 1), 1, 0};
+  Cut c = {false, std::max(T, 1), 1, 0, 0};
   if (B == 0) return c;
   const long long tiles = (long long)G * tiles_of(D / G, 64), chains = B * tiles;
   // Enough waves without a cut: one launch, a lane a channel, and a second reading
@@ -1007,12 +1024,23 @@ Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
   // 8 (2 x 2,013 x 96, N 64: 57 us with 8, 71 with 20; 1,000 x 128, N 16: 20 and 28;
   // 8,192 x 256: 42 with the 16 of 2,048 waves, 53 with 8, 43 with 20).
   c.L = (int)std::max(length(most_waves(N)), std::min(20LL, std::max(8LL, length(2048))));
+  // Of packed sequences no segment is longer than half as much again as a wave's even
+  // share of the rows (or than 64 rows), however many sequences there are: one may be
+  // nearly all of them (511 of 32 tokens and one of 48,000, 1,280 channels, N 16: 0.6 ms,
+  // 16.7 uncut; N 64: 3.0 and 81).  What even ones pay is two launches that find
+  // nothing (512 of 125 tokens: 277 us, 272 uncut; N 64: 1,177 and 1,171).
+  if (packed) {
+    const long long share = (3 * rows * tiles / (2 * most_waves(N)) + FLIGHT - 1) / FLIGHT * FLIGHT;
+    c.L = (int)std::min<long long>(c.L, std::max(64LL, share));
+    while (c.L < T && (slots_of(true, B, T, c.L) + 1) * tiles > 4 * MOST_WGS) c.L *= 2;
+  }
   if (c.L >= T) {
     c.L = T;
     return c;
   }
   c.nseg = segments_of(T, c.L);
   c.segments = slots_of(packed, B, T, c.L);
+  if (packed && c.nseg < B) c.inner = c.nseg;
   return c;
 }
 
@@ -1094,11 +1122,17 @@ void launch_outputs(const SsmParams& p, unsigned grid, bool output, hipStream_t 
 // Few states of many segments take eight threads each (20,480 states of 200
 // segments: 16 us instead of 25) or 32 (1,056 of 730: 8 instead of 19; but 6,400
 // of 485 25 instead of 15, in pieces of 32 bytes); many states keep the device busy
-// with one (245,760 of some 13 segments: 14 us, 51 with eight).
-void launch_join(const SsmParams& p, long long states, int directions, hipStream_t s) {
-  const long long each = p.segments / p.B;
+// with one (245,760 of some 13 segments: 14 us, 51 with eight).  Of more sequences
+// than places for inner segments only the cut ones are looked for, some 4,096
+// workgroups in all: most end at once (3,000 sequences of 40 tokens and 256 channels:
+// calls of 114 us, 108 without a cut, 120 with twice as many and 113 with half; with
+// 20,000 tokens behind 3,000 sequences of 5: 201, 171 and 298).
+void launch_join(const SsmParams& p, int directions, hipStream_t s) {
+  const long long DN = (long long)p.D * p.N, states = p.B * DN, each = p.segments / p.B;
   const int groups = states < 65536 && each > 64 ? states < 4096 && each > 256 ? 32 : 8 : 1;
-  const dim3 grid((unsigned)std::min(MOST_WGS, (states * groups + 255) / 256), directions);
+  const long long wgs = p.inner ? p.inner * std::max(1LL, std::min((DN + 255) / 256, 4096LL / p.inner))
+                                : std::min(MOST_WGS, (states * groups + 255) / 256);
+  const dim3 grid((unsigned)wgs, directions);
   if (groups == 32) hipLaunchKernelGGL((ssm_join_kernel<32>), grid, dim3(256), 0, s, p);
   else if (groups == 8) hipLaunchKernelGGL((ssm_join_kernel<8>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((ssm_join_kernel<1>), grid, dim3(256), 0, s, p);
@@ -1156,7 +1190,7 @@ int forward(SsmParams p, int dtype, int flags, void* workspace, long long worksp
       misaligned({p.cu, p.slots}, 4))
     return GDN_ERR_INVALID_ARG;
   Cut cut = cut_of(p.B, p.T, p.D, p.G, p.N, packed);
-  if (pooled) cut = Cut{true, std::max(p.T, 1), 1, 0};
+  if (pooled) cut = Cut{true, std::max(p.T, 1), 1, 0, 0};
   const Space w = space_of(cut.segments, 0, 0, p.D, p.G, p.N, 1, false);
   const long long need = cut.cut() ? w.bytes : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
@@ -1182,14 +1216,17 @@ int forward(SsmParams p, int dtype, int flags, void* workspace, long long worksp
   p.L = cut.L;
   p.nseg = cut.nseg;
   p.segments = cut.cut() ? cut.segments : slots_of(packed, p.B, p.T, p.L);
-  const long long wgs = p.segments * p.G * tiles_of(p.Dg, 64);
+  p.inner = cut.inner;
+  const long long tiles = (long long)p.G * tiles_of(p.Dg, 64);
+  const long long wgs = (p.inner ? (long long)p.B + p.inner : p.segments) * tiles;
   if (wgs > 4 * MOST_WGS) return GDN_ERR_INVALID_ARG;  // of 64 threads
   if (cut.cut()) {
     char* base = static_cast<char*>(workspace);
     p.E = reinterpret_cast<float*>(base + w.E);
     p.S = reinterpret_cast<float*>(base + w.S);
-    bf ? launch_outputs<__bf16>(p, (unsigned)wgs, false, s) : launch_outputs<float>(p, (unsigned)wgs, false, s);
-    launch_join(p, (long long)p.B * p.D * p.N, 1, s);
+    const unsigned first = (unsigned)((p.inner ? p.inner : p.segments) * tiles);
+    bf ? launch_outputs<__bf16>(p, first, false, s) : launch_outputs<float>(p, first, false, s);
+    launch_join(p, 1, s);
   }
   bf ? launch_outputs<__bf16>(p, (unsigned)wgs, true, s) : launch_outputs<float>(p, (unsigned)wgs, true, s);
   return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;
@@ -1284,7 +1321,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* b, const v
   if (plan.segments > 0) {
     if (bf) hipLaunchKernelGGL((ssm_bwd_maps_kernel<__bf16>), dim3((unsigned)maps), dim3(256), 0, s, p);
     else hipLaunchKernelGGL((ssm_bwd_maps_kernel<float>), dim3((unsigned)maps), dim3(256), 0, s, p);
-    launch_join(p, (long long)B * D * N, 2, s);
+    launch_join(p, 2, s);
     bf ? launch_bwd<__bf16>(p, plan.waves, (unsigned)wgs, s) : launch_bwd<float>(p, plan.waves, (unsigned)wgs, s);
   }
   // (a workgroup for 64 of the parameters' gradients, at most 4,096 more for db and dc)

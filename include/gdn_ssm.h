@@ -80,6 +80,10 @@ extern "C" {
  * launch forms the state that each segment leaves from a zero state and the
  * sum of its steps, a second joins them (h' = exp(A sum s) h + that state:
  * exact, whatever the decay), a third computes the segments from their states.
+ * Of a packed batch, whose lengths only the device knows, segments are at most
+ * one and a half of a wave's even shares of the rows long (or 64 rows), so that
+ * a long sequence among many short ones is cut too; a batch of some hundred rows
+ * is taken token by token, whole.
  *
  * Arithmetic: fp32 throughout, bf16 storage widened on load.  Non-finite
  * inputs propagate along their own channel and, through b and c, their own

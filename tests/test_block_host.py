@@ -209,6 +209,20 @@ def test_workspace_sizes_hold_over_the_range(packed):
             assert gdn.gdn_ssm_workspace_size(B, T, D, 1, 16, packed, 0, back) >= 0
 
 
+@pytest.mark.parametrize("D,G,N", [(1280, 1, 16), (1280, 1, 64), (640, 2, 32), (64, 1, 16), (33, 1, 64)])
+@pytest.mark.parametrize("T", [3000, 131072, 2 ** 30])
+def test_packed_scans_are_cut_however_many_sequences(D, G, N, T):
+    """One sequence may be nearly all of the rows: no segment is longer than one and a half of a wave's even shares of
+    them (or 64 rows), seen from the states that the workspace holds."""
+    waves = {16: 5120, 32: 4096, 64: 2048}[N]  # that the device holds at once
+    tiles = G * -(-(D // G) // 64)
+    longest = max(64, 1.5 * T * tiles / waves) + 4  # (a multiple of 4 rows)
+    for B in (1, 2, 40, 100, 300, 511, 512, 1000, 5000, 60000):
+        need = gdn.gdn_ssm_workspace_size(B, T, D, G, N, 1, 1)
+        segments = need // (4 * D * (N + 1))  # a state and a sum each; rows / L, and one for each sequence
+        assert segments - B >= int(T / longest) > 0, (B, segments)
+
+
 # ------------------------------------------------- the binding's own checks --
 
 def test_python_checks():

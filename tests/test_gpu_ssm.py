@@ -504,3 +504,76 @@ def test_gradients_of_rates_beyond_the_numbers(dtype, T):
     g = backward(t)["dA_log"]
     assert g.isfinite().all()
     assert not g[:, :2].any() and not g[3, 5].any() and g[:3, 2:].any() == (T > 0)
+
+
+# (groups of one channel: a tile of channels each, so that few channels are many waves)
+UNEVEN = [0, 0, 1, 733, 3] + [2] * 40 + [0, 65, 64, 63, 128, 300, 129] + [1] * 40 + [0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [16, 64])
+def test_uneven_packed_sequences(dtype, N):
+    """Long sequences among so many that they alone would fill the device: the long ones are cut all the same."""
+    D, rows = 48, sum(UNEVEN)
+    assert gdn.gdn_ssm_workspace_size(len(UNEVEN), rows, D, D, N, 1, 1) > 0
+    t, c = make(N, dtype, UNEVEN, D, D, N, True)
+    check_forward(t, c, dtype)
+    out, hT = forward(t)
+    h = t["h0"].clone()
+    o, h2 = forward(t, h0=h, hT=h)
+    assert h2 is h and torch.equal(o, out) and torch.equal(h, hT)
+
+
+def test_uneven_packed_sequences_with_rows_of_none():
+    """Rows before the first and behind the last sequence; the same bits without them."""
+    D, N, rows, lead, tail = 48, 16, sum(UNEVEN), 70, 90
+    t, c = make(37, "bf16", [lead] + UNEVEN[1:-1] + [tail], D, D, N, True)
+    t["cu_seqlens"], t["h0"] = t["cu_seqlens"][1:-1].contiguous(), t["h0"][1:-1].contiguous()
+    out = torch.full_like(t["x"], 77)
+    _, hT = forward(t, out=out)
+    assert (out[:lead] == 77).all() and (out[-tail:] == 77).all()
+    lens = UNEVEN[1:-1]
+    c = {**c, "h0": c["h0"][1:-1], "lens": lens, **{n: c[n][lead:-tail] for n in ("x", "dt", "b", "c", "z")}}
+    check_ssm(c, f64(out[lead:-tail]), f64(hT), "bf16", True)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_uneven_packed_offsets_that_fall_stay_inside(seed):
+    """Any offsets: what lies beside the tensors and the workspace is left."""
+    r = np.random.default_rng(seed)
+    B, D, N, T = 90, 48, 16, 1500
+    t, _ = make(38, "f32", [T], D, D, N, True)
+    offsets = r.integers(-50, T + 50, B + 1).astype(np.int32)
+    if seed == 0:
+        offsets[::2] = np.sort(offsets[::2])
+    t["cu_seqlens"], t["h0"] = torch.from_numpy(offsets).cuda(), torch.zeros(B, D, N, device="cuda")
+    whole, states = torch.full((3, T, D), 7.0, device="cuda"), torch.full((B + 2, D, N), 7.0, device="cuda")
+    need = gdn.gdn_ssm_workspace_size(B, T, D, D, N, 1, 0)
+    assert need > 0
+    ws = torch.full((3, need), 7, dtype=torch.uint8, device="cuda")
+    forward(t, out=whole[1], hT=states[1:B + 1], workspace=ws[1])
+    assert (whole[0] == 7).all() and (whole[2] == 7).all() and (states[0] == 7).all() and (states[B + 1] == 7).all()
+    assert (ws[0] == 7).all() and (ws[2] == 7).all()
+
+
+def test_uneven_packed_sequences_captured():
+    """A graph takes each replay's offsets: even, uneven, one sequence with everything."""
+    B, D, N, T = 90, 48, 16, 1440
+    t, _ = make(39, "bf16", [16] * B, D, D, N, True)
+    even = np.arange(0, T + 1, 16)
+    offsets = [even, np.concatenate([[0] * 45, [T] * 46]), np.concatenate([np.arange(45), T - 45 + np.arange(46)]),
+               np.concatenate([[5], np.sort(np.random.default_rng(1).integers(5, T, 89)), [T - 9]])]
+    forward(t)
+    torch.cuda.synchronize()
+    out, hT = torch.zeros_like(t["x"]), torch.zeros_like(t["h0"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(t, out=out, hT=hT)
+    for o in offsets:
+        t["cu_seqlens"].copy_(torch.from_numpy(o.astype(np.int32)))
+        t["x"].mul_(-1.25)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        w, wh = forward(t, out=torch.zeros_like(out))
+        assert torch.equal(out, w) and torch.equal(hT, wh)
