@@ -3,7 +3,8 @@ oracle (tolerances: block_case.py)."""
 import numpy as np
 import pytest
 
-from block_case import check_norm, check_norm_bwd, f64
+from block_case import U, check_norm, check_norm_bwd, f64, within
+from oracle import block
 
 torch = pytest.importorskip("torch")
 import gated_deltanet_recurrence_delta_amd as gdn  # noqa: E402
@@ -169,3 +170,31 @@ def test_twice_the_same():
     t, how = make(12, "f32", (3, 200), 5, 5, 64, 64, 200)
     a, b = (gdn.qk_norm_bwd(t["q"], t["k"], t["dqo"], t["dko"], **how) for _ in range(2))
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("dtype,d,rot,interleaved,tokens,Hq,Hk", [
+    ("bf16", 256, 64, False, 2600, 13, 5),   # queries two heads a unit, the last one's unit a single head
+    ("f32", 256, 256, True, 5100, 13, 2),    # four, and one
+    ("bf16", 256, 128, False, 10100, 13, 7), # eight and five; keys four and three
+    ("f32", 256, 30, False, 10100, 3, 15),   # keys eight and seven; queries one
+    ("bf16", 128, 0, False, 9400, 7, 8),     # two, keys two without a remainder
+    ("bf16", 32, 32, True, 87400, 3, 1),     # two, and one
+])
+def test_units_of_several_heads(dtype, d, rot, interleaved, tokens, Hq, Hk):
+    """A unit has 2, 4 or 8 heads from 8,192 waves of units on (d / 512 of one a head): the last of a token's units may
+    have fewer.  The weights' sums take at most 16 rows of a lane, 64 lanes of a workgroup, 2,048 / 32 workgroups and 32
+    sums of those: 176 roundings, whatever the number of rows, after a row's own d / 2 + 16."""
+    t, how = make(tokens + Hq, dtype, (tokens,), Hq, Hk, d, rot, 60)
+    if rot:
+        how["pos"][::7] = -1
+    qo, ko = gdn.qk_norm_fwd(t["q"], t["k"], **how, interleaved=interleaved)
+    g = gdn.qk_norm_bwd(t["q"], t["k"], t["dqo"], t["dko"], **how, interleaved=interleaved)
+    cos, sin, pos = (f64(how[n]) for n in ("cos", "sin", "pos"))
+    pos = None if pos is None else pos.astype(int)
+    for n, y in (("q", qo), ("k", ko)):
+        a = (f64(t[n]), f64(how["w" + n]), cos, sin, pos, False, np.float64(np.float32(1e-6)), interleaved)
+        dy = f64(t["d" + n + "o"])
+        check_norm(*a, dtype, f64(y))
+        check_norm_bwd(*a, dtype, dy, f64(g["d" + n]), None)
+        _, dw, _, mw = block.norm_bwd(*a, dy)
+        within("dw" + n, g["dw" + n], dw, (d / 2 + 16 + 176) * U * mw)
