@@ -110,8 +110,10 @@ struct Row {
 
 // --------------------------------------------------------------- functions --
 
-// 1 / (1 + exp(-x)); exp2 and the reciprocal are within 1 ulp, the product
-// with log2(e) moves the exponent by |x| 2^-24 at most.
+// 1 / (1 + exp(-x)); exp2 and the reciprocal are within 1 ulp.  The product with
+// log2(e), its rounding (1.44 |x| 2^-24) and the constant's (0.33 |x| 2^-24), moves
+// exp2's argument by up to 1.77 |x| 2^-24, the exponential by 1.23 |x| 2^-24 of itself
+// and the result by 1 / (1 + exp(x)) of that.
 __device__ static inline float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
@@ -245,8 +247,8 @@ __device__ static inline Segment sequence_of(const int32_t* cu, int T, int n) {
 // Looks for sequence n's slot among the earlier ones'.  All 64 lanes take part,
 // with one n.  The first loads are issued at once, so that a caller can issue its
 // own behind them before it asks for the answer (a token each of 512 sequences of
-// 2,560 channels: the scan 46 us, 60 with 64 slots a turn and the state's loads
-// behind the answer; the convolution 8.8 and 9.8).
+// 2,560 channels: the scan 60 us with 64 slots a turn and the state's loads behind
+// the answer, 43 so and with its states past the caches; the convolution 9.8 and 8.8).
 struct SlotSearch {
   static constexpr int MANY = 4;
   int slot, seen[MANY];

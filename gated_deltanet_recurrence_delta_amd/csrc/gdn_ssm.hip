@@ -70,7 +70,7 @@ struct SsmParams {
 
 // log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with q = e / (2
 // + e), log(1 + e) = 2 atanh(q): an odd polynomial of degree 9 in q <= 1/3,
-// fitted to 4e-9 relative.  Small steps keep their relative precision, which
+// within 8e-9 relative.  Small steps keep their relative precision, which
 // log2(1 + e) would lose.
 __device__ static inline float softplus(float v) {
   const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -LOG2E);
@@ -417,7 +417,7 @@ __device__ static inline float sum_own(const Vals<4>& v, bool odd, bool high) {
 // TURNS turns are on their way at once.
 //
 // Bound by memory for one token each (N 16: 128 sequences of 1,280 channels 7.9 us,
-// 4.7 at a large copy's rate; 512 of 2,560 channels 42 us, 37 at that rate); for
+// 4.7 at a large copy's rate; 512 of 2,560 channels 41 to 43 us, 37 at that rate); for
 // longer sequences of few channels by one wave's instructions, some 0.13 us a token.
 template <typename TI, int N, int TURNS, int TOKENS, bool STREAM>
 __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmParams p) {
@@ -631,7 +631,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_maps_kernel(const SsmParams p) {
 // again and kept in registers, and its tokens are taken backwards.
 //
 // Bound by the vector unit's instructions, three exponentials a state's update
-// among them (5,003 rows of 640 channels, N 32: 143 us, the maps 52, against 75 for
+// among them (5,003 rows of 640 channels, N 32: 138 to 146 us, the maps 52, against 71 for
 // both passes forwards).
 
 // More tokens a block need more registers, more blocks more LDS (a workgroup of
@@ -990,7 +990,8 @@ struct Cut {
 // The waves that the device's 1,024 vector units hold at once, by the states that a
 // lane keeps in registers: no more, or some units get another and the rest wait for
 // it (8 x 4,096 x 1,280, N 16: 255 us, 265 with 4,096 and 268 with 8,192; 4 x 4,096,
-// N 32: 283, 285 with 5,120; 2 x 4,096, N 64: 299, 331 with 4,096).
+// N 32: 283, 285 with 5,120; 2 x 4,096, N 64: 299, 331 with 4,096).  One sequence can
+// lose by it, by its shorter segments: 1 x 8,192 x 2,048, N 16: 124, 120 with 4,096.
 long long most_waves(int N) { return N == 16 ? 5120 : N == 32 ? 4096 : 2048; }
 
 Cut cut_of(int B, int T, int D, int G, int N, bool packed) {
@@ -1138,12 +1139,15 @@ void launch_join(const SsmParams& p, int directions, hipStream_t s) {
   else hipLaunchKernelGGL((ssm_join_kernel<1>), grid, dim3(256), 0, s, p);
 }
 
-// Two turns of four tokens in flight, one where sequences have no more, and
+// Two turns of four tokens in flight, one where sequences have no more in the mean, and
 // turns of a single token where they have that: fewer registers, more waves (one
-// token of 128 sequences, 1,280 channels: 7.9 us against 9.5).  More states than
-// the eight second-level caches hold (32 MB) then go past them, read and written
-// (1,280 channels, N 16: 512 sequences 23.3 us, 25.8 through the caches; 256
-// sequences 12.8 and 12.2).
+// token of 128 sequences, 1,280 channels: 7.9 us against 9.5).  Of packed sequences the
+// mean is all that is known: 256 of a token each 11.2 us, 16.0 with turns of four and
+// 19.9 with two of them in flight; one of 100 tokens, 156 of one and 99 empty ones 48,
+// 23.9 and 21.0, since the long one then waits for every token's loads.
+// Single tokens' states go past the eight second-level caches, read and written, where
+// they are more than those hold, 32 MB (1,280 channels, N 16: 512 sequences 23.3 us,
+// 25.8 through the caches; 256 sequences 12.8 and 12.2).
 template <typename TI, int N>
 void launch_recurrent_n(const SsmParams& p, unsigned grid, hipStream_t s) {
   const dim3 g(grid), b(256);

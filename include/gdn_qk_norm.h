@@ -65,6 +65,8 @@ extern "C" {
  * library allocates nothing and keeps no pointer.  A row's bits depend on
  * the row, its position and the weights alone.  A row of zeros with eps 0
  * gives NaN, as the formula does; non-finite values stay within their row.
+ * Squares are fp32: a row whose sum of them overflows (values of some 1e19)
+ * gives zeros, and below 1e-19 an eps of 0 can give infinities.
  */
 int gdn_qk_norm_fwd(const void* q, const void* k, const float* cos,
                     const float* sin, const int32_t* pos, const float* wq,

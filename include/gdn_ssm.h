@@ -87,8 +87,9 @@ extern "C" {
  *
  * Arithmetic: fp32 throughout, bf16 storage widened on load.  Non-finite
  * inputs propagate along their own channel and, through b and c, their own
- * token; in a cut sequence an infinite state may become NaN at a segment's
- * border where the decay over the segment is zero.
+ * token.  An infinity may come out as NaN behind its token: in a cut sequence
+ * where the decay over a segment is zero, in hT, and backwards in every
+ * gradient that it reaches.
  */
 int gdn_ssm_fwd(const void* x, const void* dt, const void* b, const void* c,
                 const float* A_log, const float* Dskip, const void* z,
